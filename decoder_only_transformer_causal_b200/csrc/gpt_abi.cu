@@ -256,14 +256,21 @@ int sync_and_read_status(void* ws, cudaStream_t s) {
 
 // One pre-LN Block ("nanoGPT 全局流程图", §2.5): x += attn(ln_1(x)); x += mlp(ln_2(x)).
 // With kv_layer set, the layer's k and v of positions [0, T) are also copied into that cache
-// ([B, block_size, 2C]) for incremental decoding.
+// ([B, block_size, 2C]) for incremental decoding.  With tree set, the T rows of a sequence are the
+// nodes of a drafted tree that attend over a cache: q, k, v go to tree->qkv.
+struct TreeBlock {
+    void* qkv;        // this layer's [B, T, 3C]
+    const void* kv;   // this layer's cache [B, block_size, 2C]
+    const int* lengths;
+    const int* parents;
+};
 int run_block(const gpt_config_t* c, const Weights& W, int l, float* x, int B, int T, uint8_t* ws,
-              const Plan& P, cudaStream_t s, void* kv_layer = nullptr) {
+              const Plan& P, cudaStream_t s, void* kv_layer = nullptr, const TreeBlock* tree = nullptr) {
     const int C = c->n_embd, nh = c->n_head, hs = C / nh;
     const int N = B * T;
     int32_t* status = status_word(ws);
     void* u = ws + P.u;
-    void* qkv = ws + P.qkv;
+    void* qkv = tree ? tree->qkv : ws + P.qkv;
     void* y = ws + P.y;
     void* h = ws + P.h;
     GPT_TRY(launch_layernorm(x, W.layer(l, W_LN1_W), W.bias(l, W_LN1_B), u, N, C, c->dtype, s));
@@ -285,7 +292,11 @@ int run_block(const gpt_config_t* c, const Weights& W, int l, float* x, int B, i
         L.y_sb = static_cast<long long>(C) * T;
         L.y_sh = hs;
         L.y_st = C;
-        GPT_TRY(launch_attention_bf16(L, B, nh, T, status, s));
+        if (tree)
+            GPT_TRY(launch_tree_attention(c->dtype, qkv, tree->kv, tree->lengths, tree->parents, y, B, T, nh, hs,
+                                          c->block_size, status, s));
+        else
+            GPT_TRY(launch_attention_bf16(L, B, nh, T, status, s));
         GPT_TRY(launch_gemm_bf16(static_cast<const bf16*>(y), C, static_cast<const bf16*>(W.layer(l, W_PROJ_W)), C,
                                  static_cast<const bf16*>(W.bias(l, W_PROJ_B)), x, C, N, C, C, GPT_EPI_RESID,
                                  c->gelu, nullptr, status, s));
@@ -314,7 +325,11 @@ int run_block(const gpt_config_t* c, const Weights& W, int l, float* x, int B, i
         L.y_sb = static_cast<long long>(C) * T;
         L.y_sh = hs;
         L.y_st = C;
-        GPT_TRY(launch_attention_f32(L, B, nh, T, hs, s));
+        if (tree)
+            GPT_TRY(launch_tree_attention(c->dtype, qkv, tree->kv, tree->lengths, tree->parents, y, B, T, nh, hs,
+                                          c->block_size, status, s));
+        else
+            GPT_TRY(launch_attention_f32(L, B, nh, T, hs, s));
         GPT_TRY(launch_linear_f32(static_cast<const float*>(y), C, static_cast<const float*>(W.layer(l, W_PROJ_W)),
                                   static_cast<const float*>(W.bias(l, W_PROJ_B)), x, C, N, C, C, GPT_EPI_RESID,
                                   c->gelu, s));
@@ -835,6 +850,128 @@ GPT_API int gpt_generate(const gpt_config_t* cfg, const void* weights, const int
     }
     if (flags & GPT_FLAG_SYNC_CHECK) return sync_and_read_status(ws, s);
     return GPT_OK;
+}
+
+// ------------------------------------------------------------------ drafted trees (tree.cu)
+namespace {
+bool tree_size_ok(int B, int N, int heads) {
+    // the largest grid is 8 CTAs per sequence and head
+    return static_cast<long long>(B) * heads <= 0x7fffffffLL / 8 && B <= 65535 && N <= GPT_TREE_MAX_NODES;
+}
+}  // namespace
+
+GPT_API int gpt_tree_attention(const void* qkv, const void* kv, const int32_t* lengths, const int32_t* parents, void* y,
+                               int B, int N, int nh, int hs, int block_size, int dtype, int32_t* status,
+                               void* stream) {
+    if (!qkv || !kv || !lengths || !parents || !y) return GPT_ERR_NULL;
+    if (B < 1 || N < 1 || nh < 1 || hs < 1 || block_size < 1) return GPT_ERR_BAD_SHAPE;
+    if (dtype != GPT_DTYPE_BF16 && dtype != GPT_DTYPE_F32) return GPT_ERR_BAD_SHAPE;
+    if (!tree_size_ok(B, N, nh)) return GPT_ERR_UNSUPPORTED;
+    if (dtype == GPT_DTYPE_BF16 ? hs != 64 : (hs % 8 || hs > 128)) return GPT_ERR_UNSUPPORTED;
+    if (nh > 0x7fffffff / 4 / hs || block_size > 0x7fffffff - 1024) return GPT_ERR_UNSUPPORTED;
+    if (!aligned(qkv, 16) || !aligned(kv, 16) || !aligned(y, 16) || !aligned(lengths, 4) || !aligned(parents, 4))
+        return GPT_ERR_BAD_ALIGN;
+    return launch_tree_attention(dtype, qkv, kv, lengths, parents, y, B, N, nh, hs, block_size, status,
+                                 static_cast<cudaStream_t>(stream));
+}
+
+GPT_API size_t gpt_tree_qkv_bytes(const gpt_config_t* cfg, int B, int N) {
+    if (validate_decode(cfg) != GPT_OK || B < 1 || N < 1 || !tree_size_ok(B, N, cfg->n_head)) return 0;
+    return static_cast<size_t>(cfg->n_layer) * B * N * 3 * cfg->n_embd * elem_size(cfg);
+}
+
+GPT_API int gpt_tree_step(const gpt_config_t* cfg, const void* weights, const int64_t* tok, const int32_t* parents,
+                          const int32_t* lengths, int B, int N, const void* kv_cache, void* tree_qkv, void* logits,
+                          void* workspace, size_t workspace_bytes, void* stream, int flags) {
+    Plan P;
+    GPT_TRY(validate_decode(cfg));
+    GPT_TRY(check_common(cfg, weights, B, N, workspace, workspace_bytes, &P));
+    if (!tok || !parents || !lengths || !kv_cache || !tree_qkv || !logits) return GPT_ERR_NULL;
+    if (!tree_size_ok(B, N, cfg->n_head)) return GPT_ERR_UNSUPPORTED;
+    if (cfg->dtype == GPT_DTYPE_BF16 && cfg->vocab_size % 8) return GPT_ERR_UNSUPPORTED;
+    if (!aligned(kv_cache, 16) || !aligned(tree_qkv, 16) || !aligned(logits, 16)) return GPT_ERR_BAD_ALIGN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    Weights W;
+    fill_weights(W, cfg, weights);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    int32_t* status = status_word(ws);
+    const int C = cfg->n_embd, V = cfg->vocab_size, R = B * N;
+    float* x = reinterpret_cast<float*>(ws + P.x);
+    void* u = ws + P.u;
+    const size_t qkv_layer = static_cast<size_t>(R) * 3 * C * elem_size(cfg);
+    GPT_TRY(cuda_status(cudaMemsetAsync(status, 0, sizeof(int32_t), s)));
+    GPT_TRY(launch_tree_embed(W.wte(), W.wpe(), tok, parents, lengths, x, B, N, C, V, cfg->block_size, cfg->dtype,
+                              status, s));
+    for (int l = 0; l < cfg->n_layer; ++l) {
+        const TreeBlock tree{static_cast<uint8_t*>(tree_qkv) + qkv_layer * l,
+                             static_cast<const uint8_t*>(kv_cache) + kv_layer_bytes(cfg, B) * l, lengths, parents};
+        GPT_TRY(run_block(cfg, W, l, x, B, N, ws, P, s, nullptr, &tree));
+    }
+    GPT_TRY(launch_layernorm(x, W.lnf_w(), W.lnf_b(), u, R, C, cfg->dtype, s));
+    if (cfg->dtype == GPT_DTYPE_BF16) {
+        GPT_TRY(launch_gemm_bf16(static_cast<const bf16*>(u), C, static_cast<const bf16*>(W.wte()), C, nullptr, logits,
+                                 V, R, V, C, GPT_EPI_STORE, cfg->gelu, nullptr, status, s));
+    } else {
+        GPT_TRY(launch_linear_f32(static_cast<const float*>(u), C, static_cast<const float*>(W.wte()), nullptr,
+                                  static_cast<float*>(logits), V, R, V, C, GPT_EPI_STORE, cfg->gelu, s));
+    }
+    if (flags & GPT_FLAG_SYNC_CHECK) return sync_and_read_status(ws, s);
+    return GPT_OK;
+}
+
+GPT_API int gpt_tree_accept(const gpt_config_t* cfg, const int32_t* parents, const int64_t* tok, const int64_t* chosen,
+                            const int32_t* lengths, int B, int N, const void* tree_qkv, void* kv_cache, int32_t* path,
+                            int32_t* n_accepted, int64_t* next_token, int32_t* lengths_out, int32_t* status,
+                            void* stream) {
+    GPT_TRY(validate_decode(cfg));
+    if (!parents || !tok || !chosen || !lengths || !tree_qkv || !kv_cache || !path || !n_accepted || !next_token ||
+        !lengths_out)
+        return GPT_ERR_NULL;
+    if (B < 1 || N < 1) return GPT_ERR_BAD_SHAPE;
+    if (!tree_size_ok(B, N, cfg->n_head)) return GPT_ERR_UNSUPPORTED;
+    const long long c_bytes = static_cast<long long>(cfg->n_embd) * elem_size(cfg);
+    if (cfg->n_layer > 0x7fffffffLL / GPT_TREE_MAX_NODES / (2 * c_bytes / 16)) return GPT_ERR_UNSUPPORTED;
+    if (!aligned(tree_qkv, 16) || !aligned(kv_cache, 16)) return GPT_ERR_BAD_ALIGN;
+    return launch_tree_accept(parents, tok, chosen, lengths, B, N, cfg->n_layer, tree_qkv, kv_cache, c_bytes,
+                              cfg->block_size, path, n_accepted, next_token, lengths_out, status,
+                              static_cast<cudaStream_t>(stream));
+}
+
+// ------------------------------------------------------------------ token log probabilities (logprobs.cu)
+namespace {
+int check_logprobs(const void* logits, long long ld, int rows, int V, int dtype, float temperature) {
+    if (!logits) return GPT_ERR_NULL;
+    if (rows < 0 || V < 1 || ld < V) return GPT_ERR_BAD_SHAPE;
+    if (dtype != GPT_DTYPE_BF16 && dtype != GPT_DTYPE_F32) return GPT_ERR_BAD_SHAPE;
+    if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature)) return GPT_ERR_BAD_SHAPE;
+    if (!aligned(logits, dtype == GPT_DTYPE_BF16 ? 2 : 4)) return GPT_ERR_BAD_ALIGN;
+    return GPT_OK;
+}
+}  // namespace
+
+GPT_API int gpt_token_logprobs(const void* logits, long long ld, const int64_t* tokens, int rows, int V, int dtype,
+                               float temperature, float* logp, float* entropy, float* lse, int k, int64_t* top_ids,
+                               float* top_logp, int32_t* status, void* stream) {
+    GPT_TRY(check_logprobs(logits, ld, rows, V, dtype, temperature));
+    if (k < 0 || k > V) return GPT_ERR_BAD_SHAPE;
+    if ((logp && !tokens) || (k > 0 && (!top_ids || !top_logp))) return GPT_ERR_NULL;
+    if (k > GPT_TOP_MAX) return GPT_ERR_UNSUPPORTED;
+    if (rows == 0) return GPT_OK;
+    return launch_logprobs(logits, ld, tokens, rows, V, dtype, temperature, logp, entropy, lse, k, top_ids, top_logp,
+                           status, static_cast<cudaStream_t>(stream));
+}
+
+GPT_API int gpt_token_logprobs_backward(const void* logits, long long ld, const int64_t* tokens, int rows, int V,
+                                        int dtype, float temperature, const float* lse, const float* entropy,
+                                        const float* dlogp, const float* dentropy, void* dlogits, long long ldd,
+                                        int32_t* status, void* stream) {
+    GPT_TRY(check_logprobs(logits, ld, rows, V, dtype, temperature));
+    if (!lse || !dlogits || (dlogp && !tokens) || (dentropy && !entropy)) return GPT_ERR_NULL;
+    if (ldd < V || (logits == dlogits && ld != ldd)) return GPT_ERR_BAD_SHAPE;
+    if (!aligned(dlogits, dtype == GPT_DTYPE_BF16 ? 2 : 4)) return GPT_ERR_BAD_ALIGN;
+    if (rows == 0) return GPT_OK;
+    return launch_logprobs_backward(logits, ld, tokens, rows, V, dtype, temperature, lse, entropy, dlogp, dentropy,
+                                    dlogits, ldd, status, static_cast<cudaStream_t>(stream));
 }
 
 // ------------------------------------------------------------------ optimizer step (optim.cu)

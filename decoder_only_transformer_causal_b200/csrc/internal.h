@@ -209,6 +209,26 @@ int sample_max_vocab();  // largest V the sampling kernel takes (the row sits in
 int launch_sample(const float* logits, long long ld_logits, int B, int V, float temperature, int top_k,
                   const float* u, int64_t* out, long long ld_out, cudaStream_t s);
 
+// ---- drafted trees (tree.cu); arguments as in gpt.h, C = nh * hs
+int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int* lengths, const int* parents, void* y,
+                          int B, int N, int nh, int hs, int block_size, int32_t* status, cudaStream_t s);
+// x[b, i, :] = wte[tok] + wpe[position of node i] (fp32 x [B, N, C]); zeros where there is no node.
+int launch_tree_embed(const void* wte, const void* wpe, const int64_t* tok, const int* parents, const int* lengths,
+                      float* x, int B, int N, int C, int V, int block_size, int dtype, int32_t* status,
+                      cudaStream_t s);
+// c_bytes: bytes of C elements (a multiple of 16).
+int launch_tree_accept(const int* parents, const int64_t* tok, const int64_t* chosen, const int* lengths, int B, int N,
+                       int n_layer, const void* tree_qkv, void* cache, long long c_bytes, int block_size, int* path,
+                       int* n_accepted, int64_t* next_token, int* lengths_out, int32_t* status, cudaStream_t s);
+
+// ---- token log probabilities (logprobs.cu); arguments as in gpt.h
+int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int rows, int V, int dtype,
+                    float temperature, float* logp, float* entropy, float* lse, int k, int64_t* top_ids,
+                    float* top_logp, int32_t* status, cudaStream_t s);
+int launch_logprobs_backward(const void* logits, long long ld, const int64_t* tokens, int rows, int V, int dtype,
+                             float temperature, const float* lse, const float* entropy, const float* dlogp,
+                             const float* dentropy, void* dlogits, long long ldd, int32_t* status, cudaStream_t s);
+
 // ---- optimizer step (optim.cu)
 constexpr int kOptMaxTensors = 1024;
 // The packed tensors in element units: tensor i spans [off[i], off[i] + numel[i]) of the flat

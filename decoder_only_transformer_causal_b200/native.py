@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
+from typing import NamedTuple
 
 import torch
 
@@ -32,6 +33,8 @@ GPT_GELU_ERF = 0
 GPT_GELU_TANH = 1
 GPT_FLAG_SYNC_CHECK = 1
 GPT_EPI_STORE, GPT_EPI_GELU, GPT_EPI_RESID = 0, 1, 2
+GPT_TREE_MAX_NODES = 64
+GPT_TOP_MAX = 64
 
 DTYPES = {"f32": GPT_DTYPE_F32, "bf16": GPT_DTYPE_BF16}
 TORCH_DTYPES = {GPT_DTYPE_F32: torch.float32, GPT_DTYPE_BF16: torch.bfloat16}
@@ -94,6 +97,12 @@ def _load() -> ctypes.CDLL:
         "gpt_decode_step": (I, [CFG, P, P, L, I, P, P, P, Z, P, I]),
         "gpt_sample": (I, [P, I, I, F, I, P, P, L, P]),
         "gpt_generate": (I, [CFG, P, P, I, I, I, F, I, P, P, P, P, P, Z, P, I]),
+        "gpt_tree_attention": (I, [P, P, P, P, P, I, I, I, I, I, D, P, P]),
+        "gpt_tree_qkv_bytes": (Z, [CFG, I, I]),
+        "gpt_tree_step": (I, [CFG, P, P, P, P, I, I, P, P, P, P, Z, P, I]),
+        "gpt_tree_accept": (I, [CFG, P, P, P, P, I, I, P, P, P, P, P, P, P, P]),
+        "gpt_token_logprobs": (I, [P, L, P, I, I, D, F, P, P, P, I, P, P, P, P]),
+        "gpt_token_logprobs_backward": (I, [P, L, P, I, I, D, F, P, P, P, P, P, L, P, P]),
         "gpt_lr_schedule": (ctypes.c_double, [L, ctypes.c_double, ctypes.c_double, L, L]),
         "gpt_param_elems": (Z, [CFG]),
         "gpt_adamw_workspace_bytes": (Z, []),
@@ -140,7 +149,8 @@ EXPORTED = ("gpt_status_string", "gpt_abi_version", "gpt_last_cuda_error", "gpt_
             "gpt_attention_train", "gpt_attention_backward_workspace_bytes", "gpt_attention_backward", "gpt_transpose",
             "gpt_linear_backward_workspace_bytes", "gpt_linear_backward",
             "gpt_train_activation_bytes", "gpt_backward_workspace_bytes", "gpt_forward_train", "gpt_backward",
-            "gpt_grad_buckets", "gpt_train_loss_terms_offset")
+            "gpt_grad_buckets", "gpt_train_loss_terms_offset", "gpt_tree_attention", "gpt_tree_qkv_bytes", "gpt_tree_step",
+            "gpt_tree_accept", "gpt_token_logprobs", "gpt_token_logprobs_backward")
 
 
 def status_string(status: int) -> str:
@@ -478,6 +488,189 @@ def generate(cfg: GPTConfig, weights: torch.Tensor, idx: torch.Tensor, max_new_t
                             _ptr(kv_cache), _ptr(workspace), workspace.numel(), _stream(stream),
                             GPT_FLAG_SYNC_CHECK if sync_check else 0), "gpt_generate")
     return out
+
+
+# ---------------------------------------------------------------- drafted trees
+def _arg(name: str, t: torch.Tensor, dtype, shape, like: torch.Tensor) -> int:
+    """The device pointer of a contiguous tensor of the given dtype and shape on like's device."""
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _on(t: torch.Tensor):
+    """Makes t's device current (the call's stream and launches belong to it)."""
+    if not t.is_cuda:
+        raise ValueError(f"expected CUDA tensors, got one on {t.device}")
+    return torch.cuda.device(t.device)
+
+
+def _status_arg(status, like):
+    return None if status is None else _arg("status", status, torch.int32, status.shape, like)
+
+
+def kv_layers(cfg: GPTConfig, kv_cache: torch.Tensor, B: int) -> torch.Tensor:
+    """The cache of alloc_kv_cache as [n_layer, B, block_size, 2, n_embd] in cfg's dtype (a view)."""
+    return kv_cache.view(cfg.torch_dtype).view(cfg.n_layer, B, cfg.block_size, 2, cfg.n_embd)
+
+
+def alloc_tree_qkv(cfg: GPTConfig, B: int, N: int, device="cuda") -> torch.Tensor:
+    """The buffer that tree_step fills and tree_accept reads: [n_layer, B, N, 3, n_embd]."""
+    if LIB.gpt_tree_qkv_bytes(ctypes.byref(cfg.c()), B, N) == 0:
+        raise GPTError(GPT_ERR_UNSUPPORTED, "gpt_tree_qkv_bytes")
+    return torch.empty((cfg.n_layer, B, N, 3, cfg.n_embd), dtype=cfg.torch_dtype, device=device)
+
+
+def tree_attention(qkv: torch.Tensor, kv: torch.Tensor, lengths: torch.Tensor, parents: torch.Tensor, n_head: int,
+                   y: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """gpt_tree_attention: qkv [B, N, 3, C], one layer's cache kv [B, block_size, 2, C], lengths int32 [B],
+    parents int32 [B, N] (-1 root, -2 no node); returns y [B, N, C]."""
+    if qkv.dim() != 4 or qkv.shape[2] != 3 or kv.dim() != 4:
+        raise ValueError("qkv must be [B, N, 3, C] and kv [B, block_size, 2, C]")
+    B, N, _, C = qkv.shape
+    if n_head < 1 or C % n_head:
+        raise ValueError("C must be a multiple of n_head")
+    with _on(qkv):
+        if y is None:
+            y = torch.empty((B, N, C), dtype=qkv.dtype, device=qkv.device)
+        _check(LIB.gpt_tree_attention(
+            _arg("qkv", qkv, qkv.dtype, (B, N, 3, C), qkv), _arg("kv", kv, qkv.dtype, (B, kv.shape[1], 2, C), qkv),
+            _arg("lengths", lengths, torch.int32, (B,), qkv), _arg("parents", parents, torch.int32, (B, N), qkv),
+            _arg("y", y, qkv.dtype, (B, N, C), qkv), B, N, n_head, C // n_head, kv.shape[1], _dt(qkv),
+            _status_arg(status, qkv), _stream(stream)), "gpt_tree_attention")
+    return y
+
+
+def tree_step(cfg: GPTConfig, weights: torch.Tensor, tok: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor,
+              kv_cache: torch.Tensor, tree_qkv: torch.Tensor, workspace: torch.Tensor,
+              logits: torch.Tensor | None = None, stream=None, sync_check: bool = False) -> torch.Tensor:
+    """gpt_tree_step: tok int64 [B, N], parents int32 [B, N], lengths int32 [B]; fills tree_qkv
+    (alloc_tree_qkv) and returns the nodes' logits [B, N, V] in cfg's dtype."""
+    B, N = tok.shape
+    with _on(tok):
+        if logits is None:
+            logits = torch.empty((B, N, cfg.vocab_size), dtype=cfg.torch_dtype, device=tok.device)
+        if kv_cache.numel() * kv_cache.element_size() < kv_cache_bytes(cfg, B):
+            raise ValueError("kv_cache is smaller than gpt_kv_cache_bytes")
+        _check(LIB.gpt_tree_step(
+            ctypes.byref(cfg.c()), _ptr(weights), _arg("tok", tok, torch.int64, (B, N), tok),
+            _arg("parents", parents, torch.int32, (B, N), tok), _arg("lengths", lengths, torch.int32, (B,), tok), B, N,
+            _ptr(kv_cache), _arg("tree_qkv", tree_qkv, cfg.torch_dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), tok),
+            _arg("logits", logits, cfg.torch_dtype, (B, N, cfg.vocab_size), tok), _ptr(workspace), workspace.numel(),
+            _stream(stream), GPT_FLAG_SYNC_CHECK if sync_check else 0), "gpt_tree_step")
+    return logits
+
+
+class TreeAccept(NamedTuple):
+    path: torch.Tensor        # int32 [B, N], -1 behind the path
+    n_accepted: torch.Tensor  # int32 [B]
+    next_token: torch.Tensor  # int64 [B], -1 for an empty path
+    lengths: torch.Tensor     # int32 [B], lengths + n_accepted
+
+
+def tree_accept(cfg: GPTConfig, parents: torch.Tensor, tok: torch.Tensor, chosen: torch.Tensor, lengths: torch.Tensor,
+                tree_qkv: torch.Tensor, kv_cache: torch.Tensor, out: TreeAccept | None = None, status=None,
+                stream=None) -> TreeAccept:
+    """gpt_tree_accept: keeps the drafted path that `chosen` confirms and copies its k, v into the cache.
+    out: buffers to write (out.lengths may be `lengths` itself)."""
+    B, N = parents.shape
+    dev = parents.device
+    with _on(parents):
+        if out is None:
+            out = TreeAccept(torch.empty((B, N), dtype=torch.int32, device=dev),
+                             torch.empty(B, dtype=torch.int32, device=dev),
+                             torch.empty(B, dtype=torch.int64, device=dev),
+                             torch.empty(B, dtype=torch.int32, device=dev))
+        if kv_cache.numel() * kv_cache.element_size() < kv_cache_bytes(cfg, B):
+            raise ValueError("kv_cache is smaller than gpt_kv_cache_bytes")
+        _check(LIB.gpt_tree_accept(
+            ctypes.byref(cfg.c()), _arg("parents", parents, torch.int32, (B, N), parents),
+            _arg("tok", tok, torch.int64, (B, N), parents), _arg("chosen", chosen, torch.int64, (B, N), parents),
+            _arg("lengths", lengths, torch.int32, (B,), parents), B, N,
+            _arg("tree_qkv", tree_qkv, cfg.torch_dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), parents), _ptr(kv_cache),
+            _arg("path", out.path, torch.int32, (B, N), parents),
+            _arg("n_accepted", out.n_accepted, torch.int32, (B,), parents),
+            _arg("next_token", out.next_token, torch.int64, (B,), parents),
+            _arg("lengths_out", out.lengths, torch.int32, (B,), parents), _status_arg(status, parents),
+            _stream(stream)), "gpt_tree_accept")
+    return out
+
+
+# ---------------------------------------------------------------- token log probabilities
+class TokenLogprobs(NamedTuple):
+    logp: torch.Tensor | None      # fp32 [rows], None without tokens
+    entropy: torch.Tensor          # fp32 [rows]
+    lse: torch.Tensor              # fp32 [rows]
+    top_ids: torch.Tensor | None   # int64 [rows, k], None for k = 0
+    top_logp: torch.Tensor | None  # fp32 [rows, k]
+
+
+def _rows(name: str, t: torch.Tensor, like: torch.Tensor):
+    """(pointer, row stride) of a [rows, V] tensor whose rows may lie apart."""
+    if t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a bfloat16 or float32 [rows, V] tensor")
+    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{name} must have the logits' shape, dtype and device")
+    rows, V = t.shape
+    if V > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the entries of a row must be contiguous")
+    ld = t.stride(0) if rows > 1 else max(V, 1)
+    if ld < V:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr() or None, ld
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: int = 0, temperature: float = 1.0,
+                   out: TokenLogprobs | None = None, status=None, stream=None) -> TokenLogprobs:
+    """gpt_token_logprobs: logits [rows, V] (bf16 or fp32; rows may lie apart, e.g. logits[:, :50257] of a
+    padded vocabulary), tokens int64 [rows] (-1: none).  out: buffers to write."""
+    ptr, ld = _rows("logits", logits, logits)
+    rows, V = logits.shape
+    with _on(logits):
+        if out is None:
+            def buf(*shape, dtype=torch.float32):
+                return torch.empty(shape, dtype=dtype, device=logits.device)
+            out = TokenLogprobs(buf(rows) if tokens is not None else None, buf(rows), buf(rows),
+                                buf(rows, k, dtype=torch.int64) if k else None, buf(rows, k) if k else None)
+
+        def opt(name, t, dtype, shape):
+            return None if t is None else _arg(name, t, dtype, shape, logits)
+        if rows:
+            _check(LIB.gpt_token_logprobs(
+                ptr, ld, opt("tokens", tokens, torch.int64, (rows,)), rows, V, _dt(logits), float(temperature),
+                opt("logp", out.logp, torch.float32, (rows,)), opt("entropy", out.entropy, torch.float32, (rows,)),
+                opt("lse", out.lse, torch.float32, (rows,)), int(k), opt("top_ids", out.top_ids, torch.int64, (rows, k)),
+                opt("top_logp", out.top_logp, torch.float32, (rows, k)), _status_arg(status, logits), _stream(stream)),
+                "gpt_token_logprobs")
+    return out
+
+
+def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, lse: torch.Tensor,
+                            entropy: torch.Tensor | None = None, dlogp: torch.Tensor | None = None,
+                            dentropy: torch.Tensor | None = None, temperature: float = 1.0,
+                            dlogits: torch.Tensor | None = None, status=None, stream=None) -> torch.Tensor:
+    """gpt_token_logprobs_backward: lse and entropy from token_logprobs; returns dlogits [rows, V] in the
+    logits' dtype (into `dlogits` when given, which may be the logits themselves)."""
+    ptr, ld = _rows("logits", logits, logits)
+    rows, V = logits.shape
+    with _on(logits):
+        if dlogits is None:
+            dlogits = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
+        dptr, ldd = _rows("dlogits", dlogits, logits)
+
+        def opt(name, t, dtype):
+            return None if t is None else _arg(name, t, dtype, (rows,), logits)
+        if rows:
+            _check(LIB.gpt_token_logprobs_backward(
+                ptr, ld, opt("tokens", tokens, torch.int64), rows, V, _dt(logits), float(temperature),
+                opt("lse", lse, torch.float32), opt("entropy", entropy, torch.float32),
+                opt("dlogp", dlogp, torch.float32), opt("dentropy", dentropy, torch.float32), dptr, ldd,
+                _status_arg(status, logits), _stream(stream)), "gpt_token_logprobs_backward")
+    return dlogits
 
 
 # ---------------------------------------------------------------- optimizer step

@@ -317,6 +317,108 @@ int gpt_generate(const gpt_config_t* cfg, const void* weights, const int64_t* id
                  int64_t* out, float* step_logits, void* kv_cache, void* workspace,
                  size_t workspace_bytes, void* stream, int flags);
 
+/* ---- drafted trees: several candidate tokens per sequence in one step -------------------
+ * The pages' generate draws one token per forward pass.  With drafted candidates (from a smaller
+ * model or a lookup) one pass scores several continuations at once and keeps the one that the
+ * model's own choices confirm; the kept tokens are those of step-by-step generation.
+ *
+ * A batch holds N <= GPT_TREE_MAX_NODES nodes per sequence, parents int32 [B, N]:
+ *   -1          a root: a token that is already certain (the last one drawn), it follows the
+ *               cached positions directly;
+ *   0 <= p < i  node i continues node p (parents come before their children);
+ *   -2          no node here (a shorter tree padded to N).
+ * Any other value, and a node whose parent is not a node, records GPT_ERR_INDEX in the status word
+ * and counts as no node.  Node i sees the cached positions [0, lengths[b]), its ancestors and itself
+ * (A(i)); it sits at position lengths[b] + |A(i)| - 1.  lengths int32 [B] lie in [0, block_size]; one
+ * outside records GPT_ERR_BAD_SHAPE and is clamped.
+ * Buffers of one layer: the cache [B, block_size, 2, C] (gpt_kv_cache_bytes' layout) and the nodes'
+ * q, k, v [B, N, 3, C], the c_attn output. */
+#define GPT_TREE_MAX_NODES 64
+
+/* Attention of the nodes over the cache and their ancestors:
+ *   y[b, i, h] = sum_j softmax_j(q[b, i, h] . k_j / sqrt(hs)) v_j,
+ *   j over cached positions [0, lengths[b]) and A(i).
+ * Rows with no node are written as zeros.  What a row does not see cannot change it: cached positions
+ * from lengths[b] on and other branches' k and v may hold any value, NaN included.
+ *   qkv     [B, N, 3, nh * hs]; kv [B, block_size, 2, nh * hs]; y [B, N, nh * hs] (no overlap with
+ *           the inputs); all in `dtype`, 16-byte aligned.
+ *   GPT_DTYPE_BF16: hs 64 (fp32 scores, statistics and sums; the probabilities are rounded to bf16 as
+ *           operands of the product with v).  GPT_DTYPE_F32: hs % 8 == 0, hs <= 128, fp32 throughout.
+ *   N = 1 with parent -1 is the attention of an ordinary decode step with a length per sequence.
+ *   status  optional device int32 (NULL allowed), never cleared by the library.
+ * No workspace; results are bit-reproducible. */
+int gpt_tree_attention(const void* qkv, const void* kv, const int32_t* lengths, const int32_t* parents,
+                       void* y, int B, int N, int nh, int hs, int block_size, int dtype,
+                       int32_t* status, void* stream);
+
+/* Bytes of the q, k, v of every layer that gpt_tree_step leaves for gpt_tree_accept: n_layer x
+ * [B, N, 3, n_embd] in the configuration's dtype.  0 on invalid arguments. */
+size_t gpt_tree_qkv_bytes(const gpt_config_t* cfg, int B, int N);
+
+/* The forward pass over a drafted tree: tok int64 [B, N], parents, lengths as above; the cache is read
+ * only.  Writes every layer's q, k, v to tree_qkv (16-byte aligned) and the logits [B, N, V] of every
+ * node in the configuration's dtype (16-byte aligned).  The logits of a node are those of the full
+ * forward over the cached tokens followed by A(i)'s, up to rounding; rows with no node hold
+ * unspecified values (their tokens are not looked at).  A node at or beyond position block_size
+ * records GPT_ERR_BAD_SHAPE and takes the last position's embedding.
+ * workspace: gpt_workspace_bytes(cfg, B, N) bytes, 256-byte aligned (N <= block_size); its status word
+ * is cleared at the start.  Configurations: those of gpt_prefill; for bf16, vocab_size % 8 == 0. */
+int gpt_tree_step(const gpt_config_t* cfg, const void* weights, const int64_t* tok, const int32_t* parents,
+                  const int32_t* lengths, int B, int N, const void* kv_cache, void* tree_qkv, void* logits,
+                  void* workspace, size_t workspace_bytes, void* stream, int flags);
+
+/* Keeps the drafted path that the model confirms.  chosen int64 [B, N]: the token drawn (gpt_sample) or
+ * taken as the largest logit at each node, i.e. the model's continuation of that node.  A root is
+ * accepted; a child is accepted when its parent is and tok[child] == chosen[parent].  The accepted node
+ * of the greatest depth (the lowest index among equals) ends the path; a path longer than the cache has
+ * room for is cut at block_size.  Writes, per sequence:
+ *   path       int32 [B, N]: the path's nodes from the root, then -1
+ *   n_accepted int32 [B]: its length (0 when no root exists or no position is free)
+ *   next_token int64 [B]: chosen at the path's last node (the next step's root), -1 for an empty path
+ *   lengths_out int32 [B]: lengths + n_accepted; may be the same array as lengths
+ * and copies the path's k and v of every layer from tree_qkv (layout of gpt_tree_step; 16-byte aligned)
+ * to the cache positions [lengths[b], lengths_out[b]); nothing else of the cache is touched.
+ * status as in gpt_tree_attention. */
+int gpt_tree_accept(const gpt_config_t* cfg, const int32_t* parents, const int64_t* tok, const int64_t* chosen,
+                    const int32_t* lengths, int B, int N, const void* tree_qkv, void* kv_cache, int32_t* path,
+                    int32_t* n_accepted, int64_t* next_token, int32_t* lengths_out, int32_t* status,
+                    void* stream);
+
+/* ---- log probabilities of given tokens --------------------------------------------------
+ * The per-position terms of "nanoGPT 全局流程图" §3.3 (logsumexp(z) - z[target]) for scoring, ranking and
+ * policy-gradient training: with z = logits[r, 0..V) / temperature and p = softmax(z),
+ *   lse[r]      = log sum_v exp(z_v)
+ *   logp[r]     = z[tokens[r]] - lse[r], 0 where tokens[r] == -1
+ *   entropy[r]  = -sum_v p_v log p_v  (0 log 0 = 0)
+ *   top_ids[r, 0..k), top_logp[r, 0..k): the k largest logits' indices, largest first, and their log
+ *               probabilities; equal logits in order of index, NaN above every number.
+ *   logits  [rows, ld] in `dtype`, the first V <= ld of each row are read (a vocabulary padded for
+ *           alignment is scored without its padding); aligned to its element.
+ *   tokens  int64 [rows] in [0, V) or -1, or NULL when logp is NULL.  Another value gives logp 0 and
+ *           GPT_ERR_INDEX in *status (optional, never cleared by the library).
+ *   logp, entropy, lse  fp32 [rows], each may be NULL.  top_ids int64 [rows, k] and top_logp fp32
+ *           [rows, k], both given or (k == 0) both NULL; 0 <= k <= min(V, GPT_TOP_MAX).
+ * Logits of -inf (forbidden tokens) have probability 0.  A row with NaN or +inf, or with nothing but
+ * -inf, has no distribution: its logp (where a token is given), entropy and top_logp are NaN.
+ * No workspace; sums in fp32 in a fixed order (bit-reproducible). */
+#define GPT_TOP_MAX 64
+int gpt_token_logprobs(const void* logits, long long ld, const int64_t* tokens, int rows, int V, int dtype,
+                       float temperature, float* logp, float* entropy, float* lse, int k, int64_t* top_ids,
+                       float* top_logp, int32_t* status, void* stream);
+
+/* Gradient of sum_r (dlogp[r] logp[r] + dentropy[r] entropy[r]) with respect to the logits:
+ *   dlogits[r, v] = (dlogp[r] ([v == tokens[r]] - p_v) - dentropy[r] p_v (log p_v + entropy[r])) / temperature
+ * lse (and, with dentropy, entropy) as gpt_token_logprobs wrote them.  dlogp NULL: no such term (tokens
+ * may be NULL); dentropy NULL: none (entropy may be NULL).  dlogp counts as 0 where tokens[r] == -1 (and
+ * where it is out of range, with GPT_ERR_INDEX).  Rows whose two factors are 0 are written as zeros and
+ * their logits are not read.  Logits of -inf get 0.
+ * dlogits [rows, ldd] in `dtype` (ldd >= V; columns from V on are left as they are); it may be the logits
+ * buffer itself with ldd == ld. */
+int gpt_token_logprobs_backward(const void* logits, long long ld, const int64_t* tokens, int rows, int V,
+                                int dtype, float temperature, const float* lse, const float* entropy,
+                                const float* dlogp, const float* dentropy, void* dlogits, long long ldd,
+                                int32_t* status, void* stream);
+
 /* ---- optimizer step -------------------------------------------------------------------
  * "nanoGPT 全局流程图", 3.5 学习率调度, 3.6 梯度裁剪 + 参数更新 and 优化器配置; "nanoGPT 代码解析",
  * configure_optimizers.  One training step's update of every parameter: the gradients are
