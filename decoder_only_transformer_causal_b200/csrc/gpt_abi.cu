@@ -943,7 +943,7 @@ int check_logprobs(const void* logits, long long ld, int rows, int V, int dtype,
     if (!logits) return GPT_ERR_NULL;
     if (rows < 0 || V < 1 || ld < V) return GPT_ERR_BAD_SHAPE;
     if (dtype != GPT_DTYPE_BF16 && dtype != GPT_DTYPE_F32) return GPT_ERR_BAD_SHAPE;
-    if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.f / temperature)) return GPT_ERR_BAD_SHAPE;
+    if (!(temperature > 0.f) || !isfinite(temperature) || !isfinite(1.5f / temperature)) return GPT_ERR_BAD_SHAPE;
     if (!aligned(logits, dtype == GPT_DTYPE_BF16 ? 2 : 4)) return GPT_ERR_BAD_ALIGN;
     return GPT_OK;
 }

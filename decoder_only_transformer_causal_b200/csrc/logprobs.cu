@@ -1,6 +1,7 @@
 // Log probabilities of given tokens, entropy and top alternatives of rows of logits, and the gradient
 // (gpt.h, gpt_token_logprobs).
 #include <math.h>
+#include <string.h>
 
 #include "common.cuh"
 #include "internal.h"
@@ -10,6 +11,13 @@ namespace gpt {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnroll = 4;          // 16-byte loads in flight per thread
+constexpr int kMaxCluster = 8;
+constexpr int kCandidates = 512;    // places for the values at or above a part's top-k bound
+constexpr int kHits = 512;          // places for the steps that reach the bound
+constexpr int kSlots = 64;          // places per thread for the maxima of its steps (of kUnroll loads)
+
+template <typename E> constexpr int kVec = 16 / sizeof(E);
 
 GPT_DEVINL float ld_act(const bf16* p) {
     return __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(p))));
@@ -18,14 +26,38 @@ GPT_DEVINL float ld_act(const float* p) { return __ldcg(p); }
 GPT_DEVINL void st(bf16* p, float v) { *p = __float2bfloat16_rn(v); }
 GPT_DEVINL void st(float* p, float v) { *p = v; }
 
-// Order-preserving key: larger value, larger key; -0 as +0, NaN above every number.
+// Maximum that keeps NaN.
+GPT_DEVINL float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+GPT_DEVINL uint32_t max2_nan(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Order-preserving key: larger value, larger key; -0 as +0, NaN above every number; key_value undoes it.
 GPT_DEVINL uint32_t order_key(float f) {
     if (f != f) return 0xffffffffu;
     const uint32_t u = __float_as_uint(f + 0.0f);
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+GPT_DEVINL float key_value(uint32_t k) { return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k); }
 
-template <typename T, typename F>
+// The key's upper half, and a value cut to its upper half (the key of the one is that half of the other's).
+GPT_DEVINL uint32_t key16(float f) { return order_key(f) >> 16; }
+GPT_DEVINL float slot_value(uint16_t h) { return __uint_as_float(static_cast<uint32_t>(h) << 16); }
+
+// A value and its column in one number that orders as the top list does: by value, equal values by
+// index.  0 stands for no entry (the lowest key is that of -inf, above 0).
+GPT_DEVINL unsigned long long entry(float z, uint32_t col) {
+    return static_cast<unsigned long long>(order_key(z)) << 32 | (0xffffffffu - col);
+}
+GPT_DEVINL uint32_t entry_col(unsigned long long e) { return 0xffffffffu - static_cast<uint32_t>(e); }
+
+template <int NT, typename T, typename F>
 GPT_DEVINL T block_reduce(T v, T* red, F op) {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
@@ -33,104 +65,526 @@ GPT_DEVINL T block_reduce(T v, T* red, F op) {
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     v = red[0];
-    for (int w = 1; w < kThreads / 32; ++w) v = op(v, red[w]);
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) v = op(v, red[w]);
     return v;
 }
 
+// The part of a row that one thread of the row's CTAs reads: the 16-byte units first, first + stride, ...
+// and at most one of the elements before the first and behind the last whole unit.
+template <typename E>
+struct Slice {
+    const E* z;
+    uint32_t head, units, ends;   // elements before the first unit, units, elements outside units
+    uint32_t stride;
+
+    GPT_DEVINL Slice(const E* row, uint32_t V, uint32_t stride_) : z(row), stride(stride_) {
+        const uint32_t mis = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(row) & 15) / sizeof(E);
+        head = mis ? kVec<E> - mis : 0;
+        if (head > V) head = V;
+        units = (V - head) / kVec<E>;
+        ends = V - units * kVec<E>;
+    }
+    GPT_DEVINL uint32_t end_col(uint32_t i) const { return i < head ? i : i + units * kVec<E>; }
+    GPT_DEVINL uint32_t unit_col(uint32_t u) const { return head + u * kVec<E>; }
+    // f(value, column) over the elements of thread `first`.
+    template <typename F>
+    GPT_DEVINL void each(uint32_t first, F f) const {
+        for (uint32_t u = first; u < units; u += stride) unit(u, f);
+        if (first < ends) f(ld_act(z + end_col(first)), end_col(first));
+    }
+    template <typename F>
+    GPT_DEVINL void unit(uint32_t u, F f) const {
+        values(__ldcg(reinterpret_cast<const uint4*>(z + unit_col(u))), unit_col(u), f);
+    }
+    template <typename F>
+    GPT_DEVINL static void values(const uint4& w, uint32_t col, F f) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (sizeof(E) == 4) {
+                f(__uint_as_float(x[i]), col + i);
+            } else {
+                f(__uint_as_float(x[i] << 16), col + 2 * i);
+                f(__uint_as_float(x[i] & 0xffff0000u), col + 2 * i + 1);
+            }
+        }
+    }
+};
+
+// Sums relative to a reference value: with e = z c - ref, c = log2(e) / T and ref = rn(c max z) (taken as
+// it is, so that its rounding cancels), the sums of 2^e and of 2^e e.  A thread's running form:
+struct Running {
+    float m, ref;
+    uint64_t s, t;   // two partial sums each
+    GPT_DEVINL void raise(float to, float c) {
+        m = max_nan(m, to);
+        const float next = m * c, d = ref - next, f = exp2_approx(d);
+        const uint64_t ff = f2_pack(f, f);
+        t = f2_mul(f2_fma(s, f2_pack(d, d), t), ff);
+        s = f2_mul(s, ff);
+        ref = next;
+    }
+    GPT_DEVINL void add2(float a, float b, uint64_t cc, uint64_t neg_ref) {
+        const uint64_t e = f2_fma(f2_pack(a, b), cc, neg_ref);
+        float e0, e1;
+        f2_unpack(e, e0, e1);
+        const uint64_t p = f2_pack(exp2_approx(e0), exp2_approx(e1));
+        s = f2_add(s, p);
+        t = f2_fma(p, e, t);
+    }
+};
+
+GPT_DEVINL float take(Running& a, const uint4 (&w)[kUnroll], float floor_z, uint32_t floor2, float c, const bf16*) {
+    uint32_t x[4 * kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) x[4 * i] = w[i].x, x[4 * i + 1] = w[i].y, x[4 * i + 2] = w[i].z, x[4 * i + 3] = w[i].w;
+    uint32_t mx = floor2;
+#pragma unroll
+    for (int i = 0; i < 4 * kUnroll; ++i) {
+        x[i] = max2_nan(x[i], floor2);
+        mx = max2_nan(mx, x[i]);
+    }
+    const float top = max_nan(__uint_as_float(mx << 16), __uint_as_float(mx & 0xffff0000u));
+    a.raise(top, c);
+    const uint64_t cc = f2_pack(c, c), ref = f2_pack(-a.ref, -a.ref);
+#pragma unroll
+    for (int i = 0; i < 4 * kUnroll; ++i)
+        a.add2(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u), cc, ref);
+    return top;
+}
+GPT_DEVINL float take(Running& a, const uint4 (&w)[kUnroll], float floor_z, uint32_t floor2, float c, const float*) {
+    float x[4 * kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+        x[4 * i] = __uint_as_float(w[i].x), x[4 * i + 1] = __uint_as_float(w[i].y);
+        x[4 * i + 2] = __uint_as_float(w[i].z), x[4 * i + 3] = __uint_as_float(w[i].w);
+    }
+    float mx = floor_z;
+#pragma unroll
+    for (int i = 0; i < 4 * kUnroll; ++i) {
+        x[i] = max_nan(x[i], floor_z);
+        mx = max_nan(mx, x[i]);
+    }
+    a.raise(mx, c);
+    const uint64_t cc = f2_pack(c, c), ref = f2_pack(-a.ref, -a.ref);
+#pragma unroll
+    for (int i = 0; i < 4 * kUnroll; i += 2) a.add2(x[i], x[i + 1], cc, ref);
+    return mx;
+}
+
+struct Part {   // one CTA's share of a row: reference, sums, and whether any value is above -inf
+    double ref;
+    float s, t;
+    int any;
+};
+
+struct ScoreArgs {
+    long long ld;
+    const int64_t* tokens;
+    uint32_t V;
+    int cluster;
+    float c, floor_z;        // log2(e) / T; the value that stands for everything at or below it
+    uint32_t floor2;         // floor_z as a pair of bf16
+    float *logp, *entropy, *lse;
+    int k;
+    int slot_shift;      // 2^slot_shift steps of a thread share a slot
+    int64_t* top_ids;
+    float* top_logp;
+    int32_t* status;
+};
+
+// A row is read once from HBM by a cluster of 1 to 8 CTAs, 16 bytes per load.
+//
+// Sums.  Each thread keeps a running maximum, raised once per 64 bytes, and the sums relative to it; the
+// threads' and then the CTAs' sums are joined in a fixed order.  Values are first raised to floor_z, so
+// that -inf needs no test in the loop (2^e is 0 and e finite); where that could show (a maximum that is
+// not finite or not far above floor_z: NaN, +-inf, rows of the type's lowest value, extreme temperatures)
+// the CTA repeats its part from L2 with a maximum first and 64-bit arguments.
+//
+// Top list.  The k-th largest of the CTA's thread maxima is a bound that at least k of its values
+// reach, and hardly more do: only the steps whose maximum reaches it (about k of them) are read
+// again, from L2.  More than 512 such values (long ties): a bisection over (value, index) finds a bound
+// that between k and 512 reach.  The values' ranks among the candidates, and across CTAs by binary
+// search in the others' lists, are their places in the list.
+template <typename E, int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
+    griddep_launch_dependents();
+    __shared__ float red[NT / 32], red_s[NT / 32], red_t[NT / 32];
+    __shared__ int ired[NT / 32];
+    __shared__ unsigned long long cand[kCandidates];
+    __shared__ unsigned long long lists[NT == 128 ? 1 : kMaxCluster][GPT_TOP_MAX];
+    __shared__ Part parts[kMaxCluster];
+    __shared__ uint16_t slots[kSlots][NT], keys[NT];
+    __shared__ uint32_t hits[kHits];
+    __shared__ uint32_t s_bound, s_hits;
+    __shared__ int s_count;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int ncta = a.cluster;
+    const int rank = ncta > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+    if (ncta > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    const long long r = blockIdx.x / ncta;
+    const Slice<E> row(logits + r * a.ld, a.V, ncta * NT);
+    const uint32_t first = rank * NT + tid;
+    griddep_wait();
+    Running run = {a.floor_z, a.floor_z * a.c, 0, 0};
+    if (a.k > 0 && a.slot_shift)
+        for (int j = 0; j < kSlots; ++j) slots[j][tid] = static_cast<uint16_t>(a.floor2);
+    uint32_t step = 0;
+    for (uint32_t u0 = first; u0 < row.units; u0 += row.stride * kUnroll, ++step) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) {
+            const uint32_t u = u0 + i * row.stride;
+            const uint32_t f = sizeof(E) == 4 ? __float_as_uint(a.floor_z) : a.floor2;
+            w[i] = u < row.units ? __ldcg(reinterpret_cast<const uint4*>(row.z + row.unit_col(u))) : make_uint4(f, f, f, f);
+        }
+        const float top = take(run, w, a.floor_z, a.floor2, a.c, row.z);
+        if (a.k > 0) {
+            uint16_t& slot = slots[step >> a.slot_shift][tid];
+            if (a.slot_shift == 0 || key16(top) > key16(slot_value(slot))) slot = static_cast<uint16_t>(__float_as_uint(top) >> 16);
+        }
+    }
+    if (first < row.ends) {
+        const float z = max_nan(ld_act(row.z + row.end_col(first)), a.floor_z);
+        run.raise(z, a.c);
+        const float e = fmaf(z, a.c, -run.ref), p = exp2_approx(e);
+        run.s = f2_add(run.s, f2_pack(p, 0.f));
+        run.t = f2_fma(f2_pack(p, 0.f), f2_pack(e, 0.f), run.t);
+    }
+
+    const uint32_t my_key = key16(run.m);
+    keys[tid] = static_cast<uint16_t>(my_key);
+    float m = run.m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[warp] = m;
+    if (tid == 0) s_count = 0, s_hits = 0;
+    __syncthreads();
+    m = red[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) m = max_nan(m, red[w]);
+    double ref = m * a.c;
+    float s, t;
+    {
+        const float d = run.ref - m * a.c, f = exp2_approx(d);
+        float s0, s1, t0, t1;
+        f2_unpack(run.s, s0, s1);
+        f2_unpack(run.t, t0, t1);
+        s0 += s1;
+        s = s0 * f;
+        t = (t0 + t1 + s0 * d) * f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+            t += __shfl_xor_sync(0xffffffffu, t, o);
+        }
+        if (lane == 0) red_s[warp] = s, red_t[warp] = t;
+    }
+    if (a.k > 0 && warp == 0) {
+        // the upper 16 bits of the k-th largest key, two bits at a time (three counts of at most 256 in one
+        // sum); 0 (every value) when fewer than k threads hold a value above floor_z
+        uint32_t mine[NT / 32];
+#pragma unroll
+        for (int j = 0; j < NT / 32; ++j) mine[j] = keys[j * 32 + lane];
+        uint32_t bound = 0;
+#pragma unroll
+        for (int bit = 14; bit >= 0; bit -= 2) {
+            const uint32_t b1 = bound | 1u << bit, b2 = bound | 2u << bit, b3 = bound | 3u << bit;
+            uint32_t above = 0;
+#pragma unroll
+            for (int j = 0; j < NT / 32; ++j)
+                above += (mine[j] >= b1 ? 1u : 0u) + (mine[j] >= b2 ? 1u << 10 : 0u) + (mine[j] >= b3 ? 1u << 20 : 0u);
+            above = __reduce_add_sync(0xffffffffu, above);
+            const uint32_t k = a.k;
+            bound = above >> 20 >= k ? b3 : (above >> 10 & 1023u) >= k ? b2 : (above & 1023u) >= k ? b1 : bound;
+        }
+        if (lane == 0) s_bound = bound <= key16(a.floor_z) ? 0 : bound;
+    }
+    __syncthreads();
+    s = red_s[0], t = red_t[0];
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) s += red_s[w], t += red_t[w];
+    int any = 1;
+    // floor_z and what it stands for are at least 2^200 times less likely than the maximum, and nothing
+    // overflows; else once more
+    if (!(fabsf(m) < 1e30f && fabsf(m) * a.c < 1e30f && (m - a.floor_z) * a.c > 200.f)) {
+        float mt = -INFINITY;
+        row.each(first, [&](float z, uint32_t) { mt = fmaxf(mt, z); });
+        m = block_reduce<NT>(mt, red, [](float x, float y) { return fmaxf(x, y); });
+        any = m > -INFINITY;
+        ref = any ? static_cast<double>(m) * a.c : 0.;   // (may pass the range of 32 bits)
+        float st = 0.f, tt = 0.f;
+        row.each(first, [&](float z, uint32_t) {
+            const float e = static_cast<float>(static_cast<double>(z) * a.c - ref), p = exp2f(e);
+            st += p;
+            tt += p == 0.f ? 0.f : p * e;
+        });
+        auto add = [](float x, float y) { return x + y; };
+        s = block_reduce<NT>(st, red, add);
+        t = block_reduce<NT>(tt, red, add);
+    }
+
+    unsigned long long* list = lists[rank];
+    if (a.k > 0) {
+        const uint32_t bound16 = s_bound;
+        const float bound = bound16 == 0 ? -INFINITY : bound16 == 0xffffu ? INFINITY : key_value(bound16 << 16);
+        auto push = [&](float z, uint32_t col) {
+            if (!(z < bound)) {
+                const int at = atomicAdd(&s_count, 1);
+                if (at < kCandidates) cand[at] = entry(z, col);
+            }
+        };
+        if (my_key >= bound16) {   // this thread's steps that reach the bound
+            const uint32_t n = (step + (1u << a.slot_shift) - 1) >> a.slot_shift;
+            for (uint32_t j = 0; j < n; ++j)
+                if (key16(slot_value(slots[j][tid])) >= bound16) {
+                    const uint32_t at = atomicAdd(&s_hits, 1u);
+                    if (at < kHits) hits[at] = j << 16 | tid;
+                }
+            if (first < row.ends) push(ld_act(row.z + row.end_col(first)), row.end_col(first));
+        }
+        __syncthreads();
+        const uint32_t n_hits = s_hits, each = static_cast<uint32_t>(kUnroll) << a.slot_shift;
+        if (n_hits <= kHits)
+            for (uint32_t i = tid; i < n_hits * each; i += NT) {   // a unit each
+                const uint32_t hit = hits[i / each];
+                const uint32_t u = rank * NT + (hit & 0xffffu) + ((hit >> 16) * each + i % each) * row.stride;
+                if (u < row.units) row.unit(u, push);
+            }
+        __syncthreads();
+        int count = s_count;
+        if (count > kCandidates || n_hits > kHits) {
+            // the largest bound over (value, index) that at least k entries reach, bit by bit until few do
+            unsigned long long at_least = 0;
+            for (int bit = 63; bit >= 0; --bit) {
+                const unsigned long long at = at_least | (1ull << bit);
+                int above = 0;
+                row.each(first, [&](float z, uint32_t col) { above += entry(z, col) >= at; });
+                above = block_reduce<NT>(above, ired, [](int x, int y) { return x + y; });
+                if (above >= a.k) {
+                    at_least = at;
+                    if (above <= kCandidates) break;
+                }
+            }
+            __syncthreads();
+            if (tid == 0) s_count = 0;
+            __syncthreads();
+            row.each(first, [&](float z, uint32_t col) {
+                const unsigned long long e = entry(z, col);
+                if (e >= at_least) cand[atomicAdd(&s_count, 1)] = e;
+            });
+            __syncthreads();
+            count = s_count;
+        }
+        // places by counting: 8 lanes per candidate
+        for (int i0 = 0; i0 < count; i0 += NT / 8) {
+            const int i = i0 + (tid >> 3);
+            const unsigned long long e = i < count ? cand[i] : 0;
+            int place = 0;
+            for (int j = tid & 7; j < count; j += 8) place += cand[j] > e;
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
+            if (i < count && (tid & 7) == 0 && place < a.k) list[place] = e;
+        }
+        if (tid >= count && tid < a.k) list[tid] = 0;   // a part shorter than k
+        __syncthreads();
+    }
+    if (ncta > 1) {
+        __syncwarp();
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");   // every CTA has started
+        if (rank != 0) {
+            if (tid < a.k) st_cluster_u64(map_to_rank(&list[tid], 0), list[tid]);
+            if (tid == 0) {
+                st_cluster_u64(map_to_rank(&parts[rank].ref, 0), __double_as_longlong(ref));
+                st_cluster_u32(map_to_rank(&parts[rank].s, 0), __float_as_uint(s));
+                st_cluster_u32(map_to_rank(&parts[rank].t, 0), __float_as_uint(t));
+                st_cluster_u32(map_to_rank(&parts[rank].any, 0), any);
+            }
+        }
+        __syncwarp();
+        cluster_sync();
+        if (rank != 0) return;
+        // the parts joined in the order of their ranks, relative to the largest reference; a part with
+        // nothing above -inf has sums of 0 (or NaN)
+        double top = any ? ref : -INFINITY;
+        for (int q = 1; q < ncta; ++q)
+            if (parts[q].any) top = any ? fmax(top, parts[q].ref) : parts[q].ref, any = 1;
+        float ss = 0.f, tt = 0.f;
+        for (int q = 0; q < ncta; ++q) {
+            const float sq = q ? parts[q].s : s, tq = q ? parts[q].t : t;
+            const double rq = q ? parts[q].ref : ref;
+            if (sq == 0.f) continue;
+            const float d = rq == top ? 0.f : static_cast<float>(rq - top), f = exp2f(d);
+            ss += sq * f;
+            if (f != 0.f) tt += (tq + sq * d) * f;
+        }
+        s = ss, t = tt, ref = any ? top : 0.;
+    }
+
+    // ---- the first CTA: the row's outputs
+    const bool none = !any && s == s;
+    const double ln2 = 0.6931471805599453, log2_s = log2f(s);
+    const float nan = __int_as_float(0x7fc00000);
+    auto logprob = [&](float z) {
+        return none ? nan : static_cast<float>((static_cast<double>(z) * a.c - ref - log2_s) * ln2);
+    };
+    if (tid == 0) {
+        if (a.lse) a.lse[r] = none ? -INFINITY : static_cast<float>((ref + log2_s) * ln2);
+        if (a.entropy) a.entropy[r] = none ? nan : static_cast<float>(ln2 * (log2_s - t / s));
+        if (a.logp) {
+            const long long tok = __ldcg(a.tokens + r);
+            float v = 0.f;
+            if (tok >= 0 && tok < a.V) v = logprob(ld_act(row.z + tok));
+            else if (tok != -1) set_status(a.status, GPT_ERR_INDEX);
+            a.logp[r] = v;
+        }
+    }
+    for (int i = tid; i < ncta * a.k; i += NT) {
+        const int q = i / a.k, j = i % a.k;
+        const unsigned long long e = lists[q][j];
+        if (e == 0) continue;
+        int place = j;
+        for (int o = 0; o < ncta; ++o) {
+            if (o == q) continue;
+            int lo = 0, hi = a.k;   // entries of list o above e
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (lists[o][mid] > e) lo = mid + 1;
+                else hi = mid;
+            }
+            place += lo;
+        }
+        if (place < a.k) {
+            const uint32_t key = static_cast<uint32_t>(e >> 32);
+            a.top_ids[r * a.k + place] = entry_col(e);
+            a.top_logp[r * a.k + place] = logprob(key == 0xffffffffu ? nan : key_value(key));
+        }
+    }
+}
+
+struct GradArgs {
+    long long ld, ldd;
+    const int64_t* tokens;
+    uint32_t V;
+    float inv_t;
+    const float *lse, *entropy, *dlogp, *dentropy;
+    int32_t* status;
+};
+
+// What a row's elements share: with l = z / T - lse, the gradient is -2^(l log2 e) (h l + gh) and g more
+// at the token's column (factors divided by T).
+struct RowGrad {
+    float inv_t, L, g, h, gh;
+    GPT_DEVINL uint64_t two(float a, float b) const {
+        // -inf: 2^-1e30 = 0, and l stays finite
+        uint64_t l = f2_fma(f2_pack(a, b), f2_pack(inv_t, inv_t), f2_pack(-L, -L));
+        float l0, l1;
+        f2_unpack(l, l0, l1);
+        l = f2_pack(fmaxf(l0, -1e30f), fmaxf(l1, -1e30f));
+        f2_unpack(f2_mul(l, f2_pack(1.4426950408889634f, 1.4426950408889634f)), l0, l1);
+        const uint64_t w = f2_fma(f2_pack(h, h), l, f2_pack(gh, gh));
+        return f2_mul(f2_pack(-exp2_approx(l0), -exp2_approx(l1)), w);
+    }
+    GPT_DEVINL float one(float z, bool hit) const {
+        float v, unused;
+        f2_unpack(two(z, z), v, unused);
+        return hit ? v + g : v;
+    }
+};
+
+GPT_DEVINL uint4 grad_unit(const RowGrad& q, const uint4& w, uint32_t hit, const bf16*) {
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    uint32_t y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a, b;
+        f2_unpack(q.two(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), a, b);
+        if (hit < 8) {   // the token's column is one of these eight
+            if (hit == 2 * i) a += q.g;
+            if (hit == 2 * i + 1) b += q.g;
+        }
+        y[i] = pack_bf16x2(a, b);
+    }
+    return make_uint4(y[0], y[1], y[2], y[3]);
+}
+GPT_DEVINL uint4 grad_unit(const RowGrad& q, const uint4& w, uint32_t hit, const float*) {
+    float y[4];
+    f2_unpack(q.two(__uint_as_float(w.x), __uint_as_float(w.y)), y[0], y[1]);
+    f2_unpack(q.two(__uint_as_float(w.z), __uint_as_float(w.w)), y[2], y[3]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (hit == i) y[i] += q.g;
+    return make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]), __float_as_uint(y[2]), __float_as_uint(y[3]));
+}
+
+// One read and one write of the row: gridDim.x CTAs share row blockIdx.y + k gridDim.y's 16-byte units.
 template <typename E>
 __global__ void __launch_bounds__(kThreads)
-    logprobs_kernel(const E* __restrict__ logits, long long ld, const int64_t* __restrict__ tokens, int V, float inv_t,
-                    float* __restrict__ logp, float* __restrict__ entropy, float* __restrict__ lse_out, int k,
-                    int64_t* __restrict__ top_ids, float* __restrict__ top_logp, int32_t* status) {
+    logprobs_backward_kernel(const E* logits, E* dlogits, long long rows, const GradArgs a) {
     griddep_launch_dependents();
     griddep_wait();
-    __shared__ float red[kThreads / 32];
-    __shared__ unsigned long long red64[kThreads / 32];
-    const long long r = blockIdx.x;
-    const E* z = logits + r * ld;
-    const int tid = threadIdx.x;
-    float m = -INFINITY;
-    for (int i = tid; i < V; i += kThreads) m = fmaxf(m, ld_act(z + i));
-    m = block_reduce(m, red, [](float a, float b) { return fmaxf(a, b); });
-    const float m0 = m == -INFINITY ? 0.f : m;
-    float s = 0.f, t = 0.f;
-    for (int i = tid; i < V; i += kThreads) {
-        const float e = (ld_act(z + i) - m0) * inv_t;
-        const float p = expf(e);
-        s += p;
-        t += p > 0.f ? p * e : (p == p ? 0.f : p);
-    }
-    auto add = [](float a, float b) { return a + b; };
-    s = block_reduce(s, red, add);
-    t = block_reduce(t, red, add);
-    const float ls = logf(s);
-    const bool none = m == -INFINITY && s == s;
-    const float nan = __int_as_float(0x7fc00000);
-    if (tid == 0) {
-        if (lse_out) lse_out[r] = none ? -INFINITY : m0 * inv_t + ls;
-        if (entropy) entropy[r] = none ? nan : ls - t / s;
-        if (logp) {
-            const long long tok = __ldcg(tokens + r);
-            float v = 0.f;
-            if (tok >= 0 && tok < V) v = none ? nan : (ld_act(z + tok) - m0) * inv_t - ls;
-            else if (tok != -1) set_status(status, GPT_ERR_INDEX);
-            logp[r] = v;
+    const uint32_t first = blockIdx.x * kThreads + threadIdx.x;
+    for (long long r = blockIdx.y; r < rows; r += gridDim.y) {
+        const Slice<E> z(logits + r * a.ld, a.V, gridDim.x * kThreads);
+        E* d = dlogits + r * a.ldd;
+        long long tok = -1;
+        float g = 0.f, h = 0.f, H = 0.f;
+        if (a.dlogp) {
+            tok = __ldcg(a.tokens + r);
+            if (tok >= 0 && tok < a.V) {
+                g = __ldcg(a.dlogp + r);
+            } else {
+                if (tok != -1 && first == 0) set_status(a.status, GPT_ERR_INDEX);
+                tok = -1;
+            }
         }
-    }
-    unsigned long long last = ~0ull;
-    for (int j = 0; j < k; ++j) {
-        unsigned long long best = 0;
-        for (int i = tid; i < V; i += kThreads) {
-            const unsigned long long key = static_cast<unsigned long long>(order_key(ld_act(z + i))) << 32 | (0xfffffffeu - i);
-            if (key < last && key > best) best = key;
+        if (a.dentropy) h = __ldcg(a.dentropy + r), H = __ldcg(a.entropy + r);
+        const float L = __ldcg(a.lse + r);
+        const Slice<E> out(d, a.V, z.stride);
+        // rows without a gradient, and those without a distribution (L - L is NaN)
+        const bool zero = (g == 0.f && h == 0.f) || L == -INFINITY;
+        if (zero || L - L != 0.f) {
+            const float v = zero ? 0.f : __int_as_float(0x7fffffff);
+            const uint32_t v2 = zero ? 0u : 0x7fff7fffu;
+            for (uint32_t u = first; u < out.units; u += out.stride)
+                *reinterpret_cast<uint4*>(d + out.unit_col(u)) = sizeof(E) == 2 ? make_uint4(v2, v2, v2, v2)
+                    : make_uint4(__float_as_uint(v), __float_as_uint(v), __float_as_uint(v), __float_as_uint(v));
+            if (first < out.ends) st(d + out.end_col(first), v);
+            continue;
         }
-        best = block_reduce(best, red64, [](unsigned long long a, unsigned long long b) { return a > b ? a : b; });
-        last = best;
-        if (tid == 0) {
-            const int id = static_cast<int>(0xfffffffeu - static_cast<uint32_t>(best));
-            top_ids[r * k + j] = id;
-            top_logp[r * k + j] = none ? nan : (ld_act(z + id) - m0) * inv_t - ls;
+        const RowGrad q = {a.inv_t, L, g * a.inv_t, h * a.inv_t, (g + h * H) * a.inv_t};
+        if (z.head == out.head) {
+            for (uint32_t u0 = first; u0 < z.units; u0 += z.stride * kUnroll) {
+                uint4 w[kUnroll];
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) {
+                    const uint32_t u = u0 + i * z.stride;
+                    if (u < z.units) w[i] = __ldcg(reinterpret_cast<const uint4*>(z.z + z.unit_col(u)));
+                }
+#pragma unroll
+                for (int i = 0; i < kUnroll; ++i) {
+                    const uint32_t u = u0 + i * z.stride;
+                    if (u < z.units)
+                        *reinterpret_cast<uint4*>(d + z.unit_col(u)) =
+                            grad_unit(q, w[i], static_cast<uint32_t>(tok) - z.unit_col(u), z.z);
+                }
+            }
+            if (first < z.ends) {
+                const uint32_t col = z.end_col(first);
+                st(d + col, q.one(ld_act(z.z + col), col == tok));
+            }
+        } else {   // rows that start at different places of a 16-byte unit
+            for (uint32_t col = first; col < a.V; col += z.stride) st(d + col, q.one(ld_act(z.z + col), col == tok));
         }
     }
 }
 
 template <typename E>
-__global__ void __launch_bounds__(kThreads)
-    logprobs_backward_kernel(const E* logits, long long ld, const int64_t* __restrict__ tokens, int V, float inv_t,
-                             const float* __restrict__ lse, const float* __restrict__ entropy,
-                             const float* __restrict__ dlogp, const float* __restrict__ dentropy, E* dlogits,
-                             long long ldd, int32_t* status) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const long long r = blockIdx.x;
-    const E* z = logits + r * ld;
-    E* d = dlogits + r * ldd;
-    long long tok = -1;
-    float g = 0.f, h = 0.f, H = 0.f;
-    if (dlogp) {
-        tok = __ldcg(tokens + r);
-        if (tok >= 0 && tok < V) {
-            g = __ldcg(dlogp + r);
-        } else {
-            if (tok != -1 && threadIdx.x == 0) set_status(status, GPT_ERR_INDEX);
-            tok = -1;
-        }
-    }
-    if (dentropy) h = __ldcg(dentropy + r), H = __ldcg(entropy + r);
-    const float L = __ldcg(lse + r);
-    const bool zero = (g == 0.f && h == 0.f) || L == -INFINITY;
-    const float bad = L - L;   // NaN for a row with no distribution, 0 otherwise
-    for (int i = threadIdx.x; i < V; i += kThreads) {
-        float v = 0.f;
-        if (!zero) {
-            const float lp = fmaxf(ld_act(z + i) * inv_t - L, -1e30f);
-            const float p = expf(lp);
-            v = -p * (g + h * (lp + H));
-            if (i == tok) v += g;
-            v = v * inv_t + bad;
-        }
-        st(d + i, v);
-    }
+int launch_score(const E* logits, const ScoreArgs& a, int rows, cudaStream_t s) {
+    if (a.cluster > 1)
+        return launch_overlapped_cluster(logprobs_kernel<E, 256>, a.cluster, dim3(rows * a.cluster), dim3(256), 0, s, logits, a);
+    return launch_overlapped(logprobs_kernel<E, 128>, dim3(rows), dim3(128), 0, s, logits, a);
 }
 
 }  // namespace
@@ -138,27 +592,48 @@ __global__ void __launch_bounds__(kThreads)
 int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int rows, int V, int dtype,
                     float temperature, float* logp, float* entropy, float* lse, int k, int64_t* top_ids,
                     float* top_logp, int32_t* status, cudaStream_t s) {
-    const float inv_t = 1.f / temperature;
-    if (dtype == GPT_DTYPE_BF16)
-        return launch_overlapped(logprobs_kernel<bf16>, dim3(rows), dim3(kThreads), 0, s,
-                                 static_cast<const bf16*>(logits), ld, tokens, V, inv_t, logp, entropy, lse, k, top_ids,
-                                 top_logp, status);
-    return launch_overlapped(logprobs_kernel<float>, dim3(rows), dim3(kThreads), 0, s,
-                             static_cast<const float*>(logits), ld, tokens, V, inv_t, logp, entropy, lse, k, top_ids,
-                             top_logp, status);
+    ScoreArgs a = {};
+    a.ld = ld;
+    a.tokens = tokens;
+    a.V = V;
+    const double c = 1.4426950408889634 / temperature;
+    a.c = static_cast<float>(c);
+    const float low = static_cast<float>(-1e30 / (c > 1. ? c : 1.));
+    uint32_t bits;
+    memcpy(&bits, &low, 4);
+    bits &= 0xffff0000u;   // a bf16 value
+    memcpy(&a.floor_z, &bits, 4);
+    a.floor2 = bits | bits >> 16;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.lse = lse;
+    a.k = k;
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.status = status;
+    int cluster = kMaxCluster;
+    while (cluster > 1 && (static_cast<long long>(rows) * cluster > 148 * 8 || V < cluster * 2048)) cluster /= 2;
+    a.cluster = cluster;
+    const long long step = static_cast<long long>(cluster > 1 ? 256 : 128) * cluster * kUnroll * (dtype == GPT_DTYPE_BF16 ? 8 : 4);
+    while ((V + step - 1) / step > static_cast<long long>(kSlots) << a.slot_shift) ++a.slot_shift;
+    return dtype == GPT_DTYPE_BF16 ? launch_score(static_cast<const bf16*>(logits), a, rows, s)
+                                   : launch_score(static_cast<const float*>(logits), a, rows, s);
 }
 
 int launch_logprobs_backward(const void* logits, long long ld, const int64_t* tokens, int rows, int V, int dtype,
                              float temperature, const float* lse, const float* entropy, const float* dlogp,
                              const float* dentropy, void* dlogits, long long ldd, int32_t* status, cudaStream_t s) {
-    const float inv_t = 1.f / temperature;
+    const GradArgs a = {ld, ldd, tokens, static_cast<uint32_t>(V), 1.f / temperature, lse, entropy, dlogp, dentropy, status};
+    // a CTA takes at least 4 units per thread; rows are split only while there are fewer than 8 CTAs per SM
+    const int per = kThreads * kUnroll * (dtype == GPT_DTYPE_BF16 ? kVec<bf16> : kVec<float>);
+    int split = 1;
+    while (static_cast<long long>(rows) * split < 148 * 8 && split * per < V) ++split;
+    const dim3 grid(split, rows < 65535 ? rows : 65535), block(kThreads);
     if (dtype == GPT_DTYPE_BF16)
-        return launch_overlapped(logprobs_backward_kernel<bf16>, dim3(rows), dim3(kThreads), 0, s,
-                                 static_cast<const bf16*>(logits), ld, tokens, V, inv_t, lse, entropy, dlogp, dentropy,
-                                 static_cast<bf16*>(dlogits), ldd, status);
-    return launch_overlapped(logprobs_backward_kernel<float>, dim3(rows), dim3(kThreads), 0, s,
-                             static_cast<const float*>(logits), ld, tokens, V, inv_t, lse, entropy, dlogp, dentropy,
-                             static_cast<float*>(dlogits), ldd, status);
+        return launch_overlapped(logprobs_backward_kernel<bf16>, grid, block, 0, s, static_cast<const bf16*>(logits),
+                                 static_cast<bf16*>(dlogits), static_cast<long long>(rows), a);
+    return launch_overlapped(logprobs_backward_kernel<float>, grid, block, 0, s, static_cast<const float*>(logits),
+                             static_cast<float*>(dlogits), static_cast<long long>(rows), a);
 }
 
 }  // namespace gpt
