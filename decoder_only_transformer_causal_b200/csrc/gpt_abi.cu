@@ -558,6 +558,7 @@ GPT_API int gpt_set_wait_limit_ns(unsigned long long ns, int force_timeout) {
     GPT_TRY(set_wait_limit_gemm(ns, force_timeout));
     GPT_TRY(set_wait_limit_head(ns, force_timeout));
     GPT_TRY(set_wait_limit_decode(ns, force_timeout));
+    GPT_TRY(set_wait_limit_tree(ns, force_timeout));
     return set_wait_limit_attention_bwd(ns, force_timeout);
 }
 

@@ -151,6 +151,7 @@ int set_wait_limit_gemm(unsigned long long ns, int force);
 int set_wait_limit_attention_bwd(unsigned long long ns, int force);
 int set_wait_limit_head(unsigned long long ns, int force);
 int set_wait_limit_decode(unsigned long long ns, int force);
+int set_wait_limit_tree(unsigned long long ns, int force);
 
 // ---- one decode step as a single cooperative kernel (decode_persistent.cu): bf16, B <= 16,
 // C % 128 == 0 and C <= 1024, head size % 8 == 0 and <= 64, V % 8 == 0, and a shared-memory plan

@@ -1,113 +1,14 @@
-// Drafted trees (gpt.h, "drafted trees"): attention of up to 64 candidate tokens per sequence over a
-// key/value cache and their ancestors, the embedding of the nodes, and the acceptance of the path
-// that the model confirms.
-#include <math.h>
-
-#include "common.cuh"
+// Drafted trees (gpt.h, "drafted trees"): the embedding of the nodes and the acceptance of the path that
+// the model confirms.  Their attention is in tree_attention.cu.
 #include "internal.h"
+#include "tree.cuh"
 
 namespace gpt {
 
 namespace {
 
-constexpr int kMaxNodes = GPT_TREE_MAX_NODES;
-
 GPT_DEVINL float to_f(bf16 v) { return __bfloat162float(v); }
 GPT_DEVINL float to_f(float v) { return v; }
-template <typename E> GPT_DEVINL E from_f(float v);
-template <> GPT_DEVINL bf16 from_f<bf16>(float v) { return __float2bfloat16_rn(v); }
-template <> GPT_DEVINL float from_f<float>(float v) { return v; }
-GPT_DEVINL float ld_act(const bf16* p) {
-    return __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(p))));
-}
-GPT_DEVINL float ld_act(const float* p) { return __ldcg(p); }
-
-// The set A(i) (node i and its ancestors) as a bit mask, 0 for no node.  par: the sequence's parents
-// in shared memory.  A parent lies below its child, so the walk ends after at most i steps.
-GPT_DEVINL unsigned long long ancestors(const int* par, int i) {
-    unsigned long long m = 0;
-    for (int j = i;;) {
-        m |= 1ull << j;
-        const int p = par[j];
-        if (p == -1) return m;
-        if (p < 0 || p >= j) return 0;
-        j = p;
-    }
-}
-
-GPT_DEVINL int clamp_length(int len, int block_size, int32_t* status) {
-    if (len >= 0 && len <= block_size) return len;
-    set_status(status, GPT_ERR_BAD_SHAPE);
-    return len < 0 ? 0 : block_size;
-}
-
-// One node and head per CTA: scores of 128 keys at a time (a key per thread), an online softmax, and
-// p.v with a dimension per thread.
-template <typename E>
-__global__ void __launch_bounds__(128)
-    tree_attention_kernel(const E* __restrict__ qkv, const E* __restrict__ kv, const int* __restrict__ lengths,
-                          const int* __restrict__ parents, E* __restrict__ y, int N, int nh, int hs, int block_size,
-                          float scale_log2, int32_t* status) {
-    griddep_launch_dependents();
-    griddep_wait();
-    __shared__ float qs[128], ps[128], red[4];
-    __shared__ int par[kMaxNodes];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int i = blockIdx.y, b = blockIdx.x / nh, h = blockIdx.x % nh;
-    const long long C = static_cast<long long>(nh) * hs;
-    const E* node = qkv + static_cast<long long>(b) * N * 3 * C + h * hs;
-    const E* cache = kv + static_cast<long long>(b) * block_size * 2 * C + h * hs;
-    if (tid < N) par[tid] = __ldcg(parents + static_cast<long long>(b) * N + tid);
-    if (tid < hs) qs[tid] = ld_act(node + i * 3 * C + tid);
-    __syncthreads();
-    const unsigned long long see = ancestors(par, i);
-    E* out = y + (static_cast<long long>(b) * N + i) * C + h * hs;
-    if (see == 0) {
-        if (tid == 0 && par[i] != -2) set_status(status, GPT_ERR_INDEX);
-        if (tid < hs) out[tid] = from_f<E>(0.f);
-        return;
-    }
-    const int len = clamp_length(__ldcg(lengths + b), block_size, status);
-    float m = -INFINITY, l = 0.f, o = 0.f;
-    for (int t0 = 0; t0 < len + N; t0 += 128) {
-        const int t = t0 + tid;
-        const bool live = t < len || (t < len + N && ((see >> (t - len)) & 1));
-        float s = -INFINITY;
-        if (live) {
-            const E* k = t < len ? cache + t * 2 * C : node + (t - len) * 3 * C + C;
-            float acc = 0.f;
-            for (int d = 0; d < hs; ++d) acc = fmaf(qs[d], ld_act(k + d), acc);
-            s = acc * scale_log2;
-        }
-        float mx = s;
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-        __syncthreads();
-        if (lane == 0) red[warp] = mx;
-        __syncthreads();
-        const float mn = fmaxf(fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])), m);
-        const float p = live ? exp2f(s - mn) : 0.f;
-        const float f = m == -INFINITY ? 0.f : exp2f(m - mn);
-        m = mn;
-        ps[tid] = p;
-        float sum = p;
-#pragma unroll
-        for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, k);
-        __syncthreads();
-        if (lane == 0) red[warp] = sum;
-        __syncthreads();
-        l = l * f + ((red[0] + red[1]) + (red[2] + red[3]));
-        o *= f;
-        if (tid < hs)
-            for (int j = 0; j < 128; ++j) {
-                const int tj = t0 + j;
-                if (!(tj < len || (tj < len + N && ((see >> (tj - len)) & 1)))) continue;
-                const E* v = tj < len ? cache + tj * 2 * C + C : node + (tj - len) * 3 * C + 2 * C;
-                o = fmaf(ps[j], ld_act(v + tid), o);
-            }
-    }
-    if (tid < hs) out[tid] = from_f<E>(o / l);
-}
 
 // x[b, i, :] = wte[tok] + wpe[lengths[b] + depth(i)], zeros where there is no node.  One node per CTA.
 template <typename E>
@@ -221,19 +122,6 @@ __global__ void __launch_bounds__(kAcceptThreads)
 }
 
 }  // namespace
-
-int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int* lengths, const int* parents, void* y,
-                          int B, int N, int nh, int hs, int block_size, int32_t* status, cudaStream_t s) {
-    const float scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(hs));
-    const dim3 grid(B * nh, N), block(128);
-    if (dtype == GPT_DTYPE_BF16)
-        return launch_overlapped(tree_attention_kernel<bf16>, grid, block, 0, s, static_cast<const bf16*>(qkv),
-                                 static_cast<const bf16*>(kv), lengths, parents, static_cast<bf16*>(y), N, nh, hs,
-                                 block_size, scale_log2, status);
-    return launch_overlapped(tree_attention_kernel<float>, grid, block, 0, s, static_cast<const float*>(qkv),
-                             static_cast<const float*>(kv), lengths, parents, static_cast<float*>(y), N, nh, hs,
-                             block_size, scale_log2, status);
-}
 
 int launch_tree_embed(const void* wte, const void* wpe, const int64_t* tok, const int* parents, const int* lengths,
                       float* x, int B, int N, int C, int V, int block_size, int dtype, int32_t* status,

@@ -1,0 +1,667 @@
+// Attention of the nodes of drafted trees over a key/value cache and their ancestors
+// (gpt.h, gpt_tree_attention):
+//   y_i = sum_j softmax_j(q_i . k_j / sqrt(hs)) v_j,  j over the cached positions and A(i).
+//
+// Per sequence and head the cached k and v are read once for all nodes, so the work is bound by HBM: 256
+// bytes (bf16) per key and head, against 4 x 64 x N operations.  A cluster of 1 to 8 CTAs takes a sequence
+// and head: its tiles of keys, the last of them the nodes' own, go round to the CTAs, each keeps an online
+// softmax (running maximum, sum and weighted values, all fp32), and the parts are joined over distributed
+// shared memory in a fixed order, so the call needs no workspace and its results are reproducible.
+#include <math.h>
+
+#include "internal.h"
+#include "tree.cuh"
+
+namespace gpt {
+
+namespace {
+
+struct TreeArgs {
+    const int* lengths;
+    const int* parents;
+    int N, nh, hs, block_size, cluster;
+    float scale_log2;   // log2(e) / sqrt(hs)
+    int32_t* status;
+};
+
+GPT_DEVINL float4 ld_cluster_f4(uint32_t cluster_addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(cluster_addr)
+                 : "memory");
+    return v;
+}
+GPT_DEVINL float2 ld_cluster_f2(uint32_t cluster_addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+GPT_DEVINL void st4(bf16* p, const float4& v) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+}
+GPT_DEVINL void st4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
+
+// Parts of a softmax over disjoint keys: weighted values o, {maximum (log2 units), sum}.  A part without
+// keys has a sum of 0 and its o is not looked at.
+struct Joined {
+    float M = -INFINITY, L = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    GPT_DEVINL void see(const float2& ml) {
+        if (ml.y != 0.f) M = fmaxf(M, ml.x);
+    }
+    GPT_DEVINL float weight(const float2& ml) const { return ml.x == M ? 1.f : exp2_approx(ml.x - M); }
+    GPT_DEVINL void add(const float2& ml, const float4& v) {
+        const float w = weight(ml);
+        L = fmaf(w, ml.y, L);
+        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    }
+};
+
+// The parts that the cluster's CTAs left at the same place of their shared memory (o [N][ld], ml [N]),
+// joined in the order of their ranks and written; each CTA takes a share of the rows' 16-byte pieces.
+// fix(i, d, v): what is added to a finished piece.
+template <typename E, typename F>
+GPT_DEVINL void join_cluster(const float* o, int ld, const float2* ml, const unsigned long long* see, const TreeArgs& a,
+                             int rank, E* y, long long row_stride, F fix) {
+    const int per = a.hs / 4;
+    for (int it = rank * blockDim.x + threadIdx.x; it < a.N * per; it += a.cluster * blockDim.x) {
+        const int i = it / per, d = (it - i * per) * 4;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (see[i]) {
+            Joined j;
+            float2 part[8];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.cluster) part[q] = ld_cluster_f2(map_to_rank(&ml[i], q)), j.see(part[q]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.cluster && part[q].y != 0.f) j.add(part[q], ld_cluster_f4(map_to_rank(&o[i * ld + d], q)));
+            const float inv = 1.f / j.L;
+            v = make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv);
+            fix(i, d, v);
+        }
+        st4(y + i * row_stride + d, v);
+    }
+}
+
+// Loads the sequence's parents and finds every node's A(i) (0: no node); all threads, ends with a barrier.
+GPT_DEVINL void load_tree(const TreeArgs& a, int b, bool report, int* par, unsigned long long* see) {
+    const int tid = threadIdx.x;
+    if (tid < a.N) par[tid] = __ldcg(a.parents + static_cast<long long>(b) * a.N + tid);
+    __syncthreads();
+    if (tid < kMaxNodes) {
+        see[tid] = tid < a.N ? ancestors(par, tid) : 0;
+        if (report && tid < a.N && see[tid] == 0 && par[tid] != -2) set_status(a.status, GPT_ERR_INDEX);
+    }
+    __syncthreads();
+}
+
+// ---------------------------------------------------------------- bf16, head size 64
+// Tiles of 128 keys by TMA (a two-deep ring), both products on the tensor cores (tcgen05):
+//   S [128 x 128] = Q' K^T, Q' the R = 32 or 64 node rows repeated 128 / R times, so that the 128 TMEM
+//     lanes are 128 / R groups of all nodes; group g uses the columns [g R, (g + 1) R) of its rows only:
+//     every thread has R scores, a row of its own, and no reduction between threads;
+//   O [128 x 64] += P V, P block-diagonal (group g's lanes hold 0 outside its columns, written once), so
+//     one chain of products accumulates every group's share, joined at the end.
+// The repeated rows cost tensor time (2 cycles per key of the 11 that its bytes take at this GPU's copy
+// rate) and save the transposes and shuffles that splitting the keys over lanes would take.
+// Warp 0 issues the loads, warp 1 the products, warps 2-5 the softmax, two CTAs share an SM.
+//
+// The product multiplies masked values by 0, so values that must not be seen are made harmless in shared
+// memory: V rows behind the sequence's end are cleared; in the nodes' tile, rows of absent nodes are
+// cleared and values that are not finite are replaced by 0 and added at the end to the rows that see them.
+namespace tc {
+constexpr int HS = 64;
+constexpr int KEYS = 128;
+constexpr int BOX = 32;                       // rows per load of the nodes' q, k, v
+constexpr int THREADS = 192;
+constexpr int TILE = KEYS * HS * 2;           // 16 KB
+constexpr int LD = HS + 4;                    // floats per row of an exported part
+constexpr int STAGES = 2;
+constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_P = 128, COL_O = 192;
+constexpr float kRescaleThreshold = 8.f;      // as in the causal kernel: P stays below 2^8
+
+struct Tail {
+    uint64_t q_full, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full, s_free, p_full, o_done, drain;
+    unsigned long long see[kMaxNodes], bad;   // bad: node rows of V with values that are not finite
+    float2 ml[KEYS], joined_ml[kMaxNodes];
+    int par[kMaxNodes];
+    uint32_t tmem;
+    int abort;
+};
+constexpr int SMEM = (1 + 2 * STAGES) * TILE + static_cast<int>(sizeof(Tail)) + 1024;
+
+template <int R>
+__global__ void __launch_bounds__(THREADS, 2)
+    tree_attention_tc(const __grid_constant__ CUtensorMap tmNode, const __grid_constant__ CUtensorMap tmCache,
+                      const bf16* __restrict__ qkv, bf16* __restrict__ y, const TreeArgs a) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t* sQ = smem;
+    uint8_t* sK = smem + TILE;
+    uint8_t* sV = sK + STAGES * TILE;
+    Tail& T = *reinterpret_cast<Tail*>(sV + STAGES * TILE);
+    volatile int* abort_flag = &T.abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int pair = static_cast<int>(blockIdx.x) / a.cluster;
+    const int b = pair / a.nh, h = pair - b * a.nh;
+
+    if (threadIdx.x == 0) {
+        uint64_t* bars = &T.q_full;
+        constexpr int n_bars = 1 + 4 * STAGES + 5;
+        for (int i = 0; i < n_bars; ++i) mbar_init(&bars[i], (&bars[i] == &T.s_free || &bars[i] == &T.p_full) ? 128u : 1u);
+        T.abort = 0;
+        T.bad = 0;
+        fence_barrier_init();
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tma_prefetch_desc(&tmNode);
+        tma_prefetch_desc(&tmCache);
+    }
+    if (warp == 1) {
+        tmem_alloc(&T.tmem, TMEM_COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = T.tmem;
+    griddep_launch_dependents();
+    griddep_wait();
+
+    const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && threadIdx.x == 0 ? a.status : nullptr);
+    const int n_cache = (len + KEYS - 1) / KEYS;   // tiles of the cache; tile n_cache is the nodes'
+    const int n_steps = rank <= n_cache ? (n_cache - rank) / a.cluster + 1 : 0;
+    const bool has_nodes = n_cache % a.cluster == rank;   // as the last step
+
+    if (warp == 0) {
+        // ------------------------------------------------------------ loads
+        if (lane == 0 && n_steps > 0) {
+            mbar_arrive_expect_tx(&T.q_full, TILE);
+            for (int i = 0; i < KEYS / BOX; ++i)
+                tma_load_4d(sQ + i * (BOX * HS * 2), &tmNode, &T.q_full, 0, h, (i * BOX) % R, b);
+            int issued_k = 0, issued_v = 0;
+            for (int j = 0; j < n_steps; ++j) {
+                const int st = j % STAGES;
+                const uint32_t ph = (j / STAGES) & 1;
+                const int t = rank + j * a.cluster;
+                for (int v = 0; v < 2; ++v) {
+                    uint64_t* full = v ? &T.v_full[st] : &T.k_full[st];
+                    uint8_t* dst = (v ? sV : sK) + st * TILE;
+                    if (!mbar_wait(v ? &T.v_empty[st] : &T.k_empty[st], ph ^ 1u, abort_flag)) {
+                        j = n_steps;
+                        break;
+                    }
+                    if (t < n_cache) {
+                        mbar_arrive_expect_tx(full, TILE);
+                        tma_load_4d(dst, &tmCache, full, 0, v * a.nh + h, t * KEYS, b);
+                    } else {
+                        mbar_arrive_expect_tx(full, R * HS * 2);
+                        for (int i = 0; i < R / BOX; ++i)
+                            tma_load_4d(dst + i * (BOX * HS * 2), &tmNode, full, 0, (1 + v) * a.nh + h, i * BOX, b);
+                    }
+                    ++(v ? issued_v : issued_k);
+                }
+            }
+            // No bulk copy may still target shared memory when the CTA exits.
+            mbar_drain(&T.q_full, 0);
+            for (int i = 1; i <= STAGES; ++i) {
+                if (issued_k >= i) mbar_drain(&T.k_full[(issued_k - i) % STAGES], ((issued_k - i) / STAGES) & 1);
+                if (issued_v >= i) mbar_drain(&T.v_full[(issued_v - i) % STAGES], ((issued_v - i) / STAGES) & 1);
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------ products
+        if (lane == 0 && n_steps > 0) {
+            constexpr uint32_t idesc_s = make_idesc_bf16(128, KEYS, false), idesc_sn = make_idesc_bf16(128, R, false);
+            constexpr uint32_t idesc_o = make_idesc_bf16(128, HS, true);
+            const uint32_t tS = tmem + COL_S, tP = tmem + COL_P, tO = tmem + COL_O;
+            // Testing aid (gpt_set_wait_limit_ns): nothing arrives on `drain` before the commit below.
+            if (g_force_timeout) mbar_wait(&T.drain, 0, abort_flag);
+            const bool ok = !g_force_timeout && mbar_wait(&T.q_full, 0, abort_flag);
+            tc_fence_after();
+            const uint32_t q_addr = smem_addr(sQ);
+            for (int j = 0; ok && j <= n_steps; ++j) {
+                if (j < n_steps) {   // S_j, once the softmax has taken S_{j-1} out of TMEM
+                    const int st = j % STAGES;
+                    if (!mbar_wait(&T.k_full[st], (j / STAGES) & 1, abort_flag)) break;
+                    if (j > 0 && !mbar_wait(&T.s_free, (j - 1) & 1, abort_flag)) break;
+                    tc_fence_after();
+                    const uint32_t k_addr = smem_addr(sK + st * TILE);
+                    const uint32_t idesc = has_nodes && j == n_steps - 1 ? idesc_sn : idesc_s;
+#pragma unroll
+                    for (int kk = 0; kk < HS / 16; ++kk)
+                        umma_ss(tS, make_sdesc_sw128(q_addr + kk * 32), make_sdesc_sw128(k_addr + kk * 32), idesc, kk > 0);
+                    umma_commit(&T.k_empty[st]);
+                    umma_commit(&T.s_full);
+                }
+                if (j > 0) {         // O += P_{j-1} V_{j-1}, once the softmax has written P_{j-1}
+                    const int jj = j - 1, st = jj % STAGES;
+                    if (!mbar_wait(&T.p_full, jj & 1, abort_flag)) break;
+                    if (!mbar_wait(&T.v_full[st], (jj / STAGES) & 1, abort_flag)) break;
+                    tc_fence_after();
+                    const uint32_t v_addr = smem_addr(sV + st * TILE);
+                    const int n_k = has_nodes && jj == n_steps - 1 ? R / 16 : KEYS / 16;
+                    for (int kk = 0; kk < n_k; ++kk)
+                        umma_ts(tO, tP + kk * 8, make_sdesc_sw128(v_addr + kk * 2048), idesc_o, jj > 0 || kk > 0);
+                    umma_commit(&T.v_empty[st]);
+                    umma_commit(&T.o_done);
+                }
+            }
+            umma_commit(&T.drain);
+            mbar_drain(&T.drain, 0);
+        }
+    }
+    // every node's A(i), while the first tiles travel (the issuing lanes pass through when they are done)
+    if (warp >= 2) {
+        const int t = threadIdx.x - 64;
+        if (t < a.N) T.par[t] = __ldcg(a.parents + static_cast<long long>(b) * a.N + t);
+        named_barrier(1, 128);
+        if (t < kMaxNodes) {
+            T.see[t] = t < a.N ? ancestors(T.par, t) : 0;
+            if (h == 0 && rank == 0 && t < a.N && T.see[t] == 0 && T.par[t] != -2) set_status(a.status, GPT_ERR_INDEX);
+        }
+        named_barrier(1, 128);
+
+        // ------------------------------------------------------------ softmax
+        const int quarter = warp & 3;
+        const int r = quarter * 32 + lane, group = r / R, node = r % R, col0 = group * R;
+        const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
+        const uint32_t tS = tmem + COL_S + lane_off + col0, tP = tmem + COL_P + lane_off, tO = tmem + COL_O + lane_off;
+        const unsigned long long see = T.see[node];
+        float m_used = -INFINITY, l = 0.f;
+        bool ok = n_steps > 0;
+        if (ok) {
+            uint32_t zero[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) zero[i] = 0;
+            tmem_st32(tP, zero);
+            tmem_st32(tP + 32, zero);
+        }
+        for (int j = 0; ok && j < n_steps; ++j) {
+            const bool nodes = has_nodes && j == n_steps - 1;
+            const int st = j % STAGES;
+            const int keys = nodes ? R : len - (rank + j * a.cluster) * KEYS;   // of this tile
+            if (nodes || keys < KEYS) {
+                // V rows that must not matter
+                const bool got = mbar_wait(&T.v_full[st], (j / STAGES) & 1, abort_flag);
+                uint4* row = reinterpret_cast<uint4*>(sV + st * TILE + r * (HS * 2));
+                if (got && (nodes ? r < R && T.see[r & (kMaxNodes - 1)] == 0 : r >= keys)) {
+#pragma unroll
+                    for (int i = 0; i < HS / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                } else if (got && nodes && r < R) {
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < HS / 8; ++i) {
+                        uint32_t w[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
+                        bool here = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, here = true;
+                            if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, here = true;
+                        }
+                        if (here) row[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                        any |= here;
+                    }
+                    if (any) atomicOr(&T.bad, 1ull << r);
+                }
+                fence_proxy_async_shared();
+            }
+            const bool got = mbar_wait(&T.s_full, j & 1, abort_flag);
+            __syncwarp();   // tcgen05.ld / st are warp-collective
+            if (!__all_sync(0xffffffffu, got)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            float s[R];
+            {
+                uint32_t u[R];
+                if constexpr (R == 32) tmem_ld32(tS, u);
+                else tmem_ld64(tS, u);
+#pragma unroll
+                for (int c = 0; c < R; ++c) s[c] = __uint_as_float(u[c]);
+            }
+            tc_fence_before();
+            mbar_arrive(&T.s_free);
+            const bool idle = nodes && group > 0;   // (warp-uniform)
+            uint32_t pk[R / 2];
+            float alpha = 1.f;
+            if (!idle) {
+                if (nodes) {
+#pragma unroll
+                    for (int c = 0; c < R; ++c)
+                        if (!((see >> c) & 1)) s[c] = -INFINITY;
+                } else if (keys - col0 < R) {
+#pragma unroll
+                    for (int c = 0; c < R; ++c)
+                        if (c >= keys - col0) s[c] = -INFINITY;
+                }
+                float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                for (int c = 4; c < R; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
+                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                if (mx > m_used + kRescaleThreshold || (m_used == -INFINITY && mx > -INFINITY)) {
+                    alpha = m_used == -INFINITY ? 0.f : exp2_approx(m_used - mx);
+                    m_used = mx;
+                }
+                const float off = m_used == -INFINITY ? 0.f : -m_used;   // nothing visible yet: 2^-inf
+                const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), off2 = f2_pack(off, off);
+                uint64_t acc[2] = {0, 0};
+#pragma unroll
+                for (int c = 0; c < R; c += 2) {
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, off2), x0, x1);
+                    const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
+                    acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
+                    pk[c / 2] = pack_bf16x2(p0, p1);
+                }
+                float a0, a1;
+                f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
+                l = l * alpha + (a0 + a1);
+            }
+            // P_j may overwrite P_{j-1} and O may be rescaled only after O += P_{j-1} V_{j-1}.
+            if (j > 0) {
+                const bool done = mbar_wait(&T.o_done, (j - 1) & 1, abort_flag);
+                __syncwarp();
+                if (!__all_sync(0xffffffffu, done)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+            }
+            if (!idle) {
+                if constexpr (R == 32) tmem_st16(tP + group * (R / 2), pk);
+                else tmem_st32(tP + group * (R / 2), pk);
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+                    for (int c = 0; c < HS; c += 32) {
+                        uint32_t u[32];
+                        tmem_ld32(tO + c, u);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * alpha);
+                        tmem_st32(tO + c, u);
+                    }
+                }
+            }
+            tc_fence_before();
+            mbar_arrive(&T.p_full);
+        }
+        const bool last = ok && mbar_wait(&T.o_done, (n_steps - 1) & 1, abort_flag);
+        __syncwarp();
+        float* out = reinterpret_cast<float*>(sK) + r * LD;   // every tile has been consumed
+        const bool done = __all_sync(0xffffffffu, last);
+        if (done) {
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < HS; c += 32) {
+                uint32_t u[32];
+                tmem_ld32(tO + c, u);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+            }
+        }
+        T.ml[r] = make_float2(m_used, done ? l : 0.f);
+        tc_fence_before();
+    }
+
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc(tmem, TMEM_COLS);
+    }
+    // The groups joined within the CTA, then the CTAs.
+    const float* parts = reinterpret_cast<const float*>(sK);
+    float* joined = reinterpret_cast<float*>(sK) + KEYS * LD;
+    for (int it = threadIdx.x; it < a.N * (HS / 4); it += THREADS) {
+        const int i = it / (HS / 4), d = it % (HS / 4) * 4;
+        Joined j;
+#pragma unroll
+        for (int g = 0; g < KEYS / R; ++g) j.see(T.ml[g * R + i]);
+#pragma unroll
+        for (int g = 0; g < KEYS / R; ++g)
+            if (T.ml[g * R + i].y != 0.f)
+                j.add(T.ml[g * R + i], *reinterpret_cast<const float4*>(parts + (g * R + i) * LD + d));
+        *reinterpret_cast<float4*>(joined + i * LD + d) = j.o;
+        if (d == 0) T.joined_ml[i] = make_float2(j.M, j.L);
+    }
+    cluster_sync();
+    const unsigned long long bad = static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&T.bad) + 1, n_cache % a.cluster))) << 32 |
+                                   ld_cluster_u32(map_to_rank(&T.bad, n_cache % a.cluster));
+    const long long C = static_cast<long long>(a.nh) * HS;
+    join_cluster(joined, LD, T.joined_ml, T.see, a, rank, y + static_cast<long long>(b) * a.N * C + h * HS, C,
+                 [&](int i, int d, float4& v) {
+                     for (unsigned long long todo = bad & T.see[i]; todo; todo &= todo - 1) {
+                         const bf16* w = qkv + (static_cast<long long>(b) * a.N + __ffsll(todo) - 1) * 3 * C + 2 * C + h * HS + d;
+                         float* x = &v.x;
+                         for (int e = 0; e < 4; ++e) {
+                             const float f = __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(w + e))));
+                             if (!isfinite(f)) x[e] += f;
+                         }
+                     }
+                 });
+    if (threadIdx.x == 0 && *abort_flag) set_status(a.status, GPT_ERR_TIMEOUT);
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while another reads its part
+}
+}  // namespace tc
+
+// ---------------------------------------------------------------- fp32, head size 8 to 128
+// The same split in CUDA cores: tiles of 64 keys in shared memory, a thread has NB / 8 nodes x 4 keys of
+// the scores and NB / 8 nodes x hs / 16 dimensions of the values.
+namespace simt {
+constexpr int THREADS = 128;
+constexpr int KEYS = 64;
+
+GPT_DEVINL void cp_async16(void* dst, const void* src, int src_bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(src_bytes) : "memory");
+}
+GPT_DEVINL void cp_async_wait_all() { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory"); }
+
+constexpr int smem_floats(int nb, int hs) { return (nb + 2 * KEYS) * (hs + 4) + nb * (KEYS + 4); }
+
+template <int NB>
+__global__ void __launch_bounds__(THREADS)
+    tree_attention_f32(const float* __restrict__ qkv, const float* __restrict__ kv, float* __restrict__ y, const TreeArgs a) {
+    constexpr int RN = NB / 8;
+    extern __shared__ __align__(16) float sm[];
+    __shared__ unsigned long long see[kMaxNodes];
+    __shared__ int par[kMaxNodes];
+    __shared__ float2 ml[NB];
+    const int hs = a.hs, ld = hs + 4, N = a.N;
+    float* sQ = sm;
+    float* sK = sQ + NB * ld;
+    float* sV = sK + KEYS * ld;
+    float* sP = sV + KEYS * ld;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int rank = static_cast<int>(cluster_ctarank());
+    const int pair = static_cast<int>(blockIdx.x) / a.cluster;
+    const int b = pair / a.nh, h = pair - b * a.nh;
+    const long long C = static_cast<long long>(a.nh) * hs;
+    const float* node = qkv + static_cast<long long>(b) * N * 3 * C + h * hs;
+    const float* cache = kv + static_cast<long long>(b) * a.block_size * 2 * C + h * hs;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && tid == 0 ? a.status : nullptr);
+    const int n_cache = (len + KEYS - 1) / KEYS;
+    const int per = hs / 4;
+    for (int it = tid; it < NB * per; it += THREADS) {
+        const int i = it / per, d = (it - i * per) * 4;
+        cp_async16(sQ + i * ld + d, node + (i < N ? i * 3 * C + d : 0), i < N ? 16 : 0);
+    }
+    load_tree(a, b, h == 0 && rank == 0, par, see);
+
+    float o[RN][8], m[RN], l[RN];
+#pragma unroll
+    for (int i = 0; i < RN; ++i) {
+        m[i] = -INFINITY, l[i] = 0.f;
+#pragma unroll
+        for (int d = 0; d < 8; ++d) o[i][d] = 0.f;
+    }
+    for (int t = rank; t <= n_cache; t += a.cluster) {
+        const bool nodes = t == n_cache;
+        const int keys = nodes ? N : min(KEYS, len - t * KEYS);
+        __syncthreads();
+        for (int it = tid; it < KEYS * per; it += THREADS) {
+            const int k = it / per, d = (it - k * per) * 4;
+            const float* src = nodes ? node + k * 3 * C + C + d : cache + (static_cast<long long>(t) * KEYS + k) * 2 * C + d;
+            const bool in = k < keys;
+            cp_async16(sK + k * ld + d, in ? src : node, in ? 16 : 0);
+            cp_async16(sV + k * ld + d, in ? src + C : node, in ? 16 : 0);
+        }
+        cp_async_wait_all();
+        __syncthreads();
+        float s[RN][4];
+#pragma unroll
+        for (int i = 0; i < RN; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
+        for (int d = 0; d < hs; d += 4) {
+            float4 kk[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) kk[k] = *reinterpret_cast<const float4*>(sK + (tx + 16 * k) * ld + d);
+#pragma unroll
+            for (int i = 0; i < RN; ++i) {
+                const float4 q = *reinterpret_cast<const float4*>(sQ + (ty * RN + i) * ld + d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    s[i][k] = fmaf(q.x, kk[k].x, fmaf(q.y, kk[k].y, fmaf(q.z, kk[k].z, fmaf(q.w, kk[k].w, s[i][k]))));
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RN; ++i) {
+            const unsigned long long mine = see[ty * RN + i];
+            float mx = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int key = tx + 16 * k;
+                const bool live = nodes ? (mine >> key) & 1 : key < keys;
+                s[i][k] = live ? s[i][k] * a.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, s[i][k]);
+            }
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
+            mx = fmaxf(mx, m[i]);
+            const float off = mx == -INFINITY ? 0.f : mx;
+            const float alpha = m[i] == mx ? 1.f : exp2f(m[i] - off);
+            m[i] = mx;
+            float sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float p = exp2f(s[i][k] - off);
+                sP[(ty * RN + i) * (KEYS + 4) + tx + 16 * k] = p;
+                sum += p;
+            }
+#pragma unroll
+            for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+            l[i] = l[i] * alpha + sum;
+#pragma unroll
+            for (int d = 0; d < 8; ++d) o[i][d] *= alpha;
+        }
+        __syncwarp();   // a node's weights are written and read by the same half warp
+        for (int k = 0; k < KEYS; k += 4) {
+            float4 p[RN];
+#pragma unroll
+            for (int i = 0; i < RN; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * RN + i) * (KEYS + 4) + k);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                float4 v[2];
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                    v[g] = tx * 4 + 64 * g < hs ? *reinterpret_cast<const float4*>(sV + (k + x) * ld + tx * 4 + 64 * g)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < RN; ++i) {
+                    // another branch's value may be NaN: it is not even multiplied by 0
+                    if (nodes && !((see[ty * RN + i] >> (k + x)) & 1)) continue;
+                    const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        o[i][4 * g] = fmaf(w, v[g].x, o[i][4 * g]);
+                        o[i][4 * g + 1] = fmaf(w, v[g].y, o[i][4 * g + 1]);
+                        o[i][4 * g + 2] = fmaf(w, v[g].z, o[i][4 * g + 2]);
+                        o[i][4 * g + 3] = fmaf(w, v[g].w, o[i][4 * g + 3]);
+                    }
+                }
+            }
+        }
+    }
+    cp_async_wait_all();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < RN; ++i) {
+#pragma unroll
+        for (int g = 0; g < 2; ++g)
+            if (tx * 4 + 64 * g < hs)
+                *reinterpret_cast<float4*>(sK + (ty * RN + i) * ld + tx * 4 + 64 * g) =
+                    make_float4(o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]);
+        if (tx == 0) ml[ty * RN + i] = make_float2(m[i], l[i]);
+    }
+    __syncthreads();
+    cluster_sync();
+    join_cluster(sK, ld, ml, see, a, rank, y + static_cast<long long>(b) * N * C + h * hs, C, [](int, int, float4&) {});
+    __syncwarp();
+    cluster_sync();
+}
+}  // namespace simt
+
+}  // namespace
+
+int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int* lengths, const int* parents, void* y,
+                          int B, int N, int nh, int hs, int block_size, int32_t* status, cudaStream_t s) {
+    TreeArgs a = {};
+    a.lengths = lengths;
+    a.parents = parents;
+    a.N = N;
+    a.nh = nh;
+    a.hs = hs;
+    a.block_size = block_size;
+    a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(hs)));
+    a.status = status;
+    const bool f32 = dtype == GPT_DTYPE_F32;
+    const long long pairs = static_cast<long long>(B) * nh;
+    const int tiles = (block_size - 1) / (f32 ? simt::KEYS : tc::KEYS) + 2;
+    a.cluster = 1;
+    while (a.cluster < 8 && pairs * a.cluster < 148 * 8 && a.cluster < tiles) a.cluster *= 2;
+    const dim3 grid(static_cast<unsigned>(pairs * a.cluster));
+    int rc;
+    if (f32) {
+        const size_t smem = sizeof(float) * simt::smem_floats(N <= 16 ? 16 : 64, hs);
+        static size_t opted16[kMaxDevices] = {}, opted64[kMaxDevices] = {};
+        auto kern = N <= 16 ? simt::tree_attention_f32<16> : simt::tree_attention_f32<64>;
+        rc = N <= 16 ? opt_in_smem(reinterpret_cast<const void*>(kern), smem, opted16)
+                     : opt_in_smem(reinterpret_cast<const void*>(kern), smem, opted64);
+        if (rc) return rc;
+        return launch_overlapped_cluster(kern, a.cluster, grid, dim3(simt::THREADS), smem, s,
+                                         static_cast<const float*>(qkv), static_cast<const float*>(kv),
+                                         static_cast<float*>(y), a);
+    }
+    // {hs, heads of q, k, v (nodes) or k, v (cache), rows, sequences}
+    const uint64_t C2 = static_cast<uint64_t>(nh) * hs * 2;
+    const uint64_t node_dims[4] = {64, static_cast<uint64_t>(3) * nh, static_cast<uint64_t>(N), static_cast<uint64_t>(B)};
+    const uint64_t node_strides[3] = {128, 3 * C2, 3 * C2 * N};
+    const uint32_t node_box[4] = {64, 1, tc::BOX, 1};
+    const uint64_t cache_dims[4] = {64, static_cast<uint64_t>(2) * nh, static_cast<uint64_t>(block_size), static_cast<uint64_t>(B)};
+    const uint64_t cache_strides[3] = {128, 2 * C2, 2 * C2 * block_size};
+    const uint32_t cache_box[4] = {64, 1, tc::KEYS, 1};
+    CUtensorMap node_map, cache_map;
+    rc = make_tmap_bf16_4d(&node_map, qkv, node_dims, node_strides, node_box);
+    if (!rc) rc = make_tmap_bf16_4d(&cache_map, kv, cache_dims, cache_strides, cache_box);
+    if (rc) return rc;
+    static size_t opted32[kMaxDevices] = {}, opted64[kMaxDevices] = {};
+    auto kern = N <= 32 ? tc::tree_attention_tc<32> : tc::tree_attention_tc<64>;
+    rc = N <= 32 ? opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted32)
+                 : opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted64);
+    if (rc) return rc;
+    return launch_overlapped_cluster(kern, a.cluster, grid, dim3(tc::THREADS), tc::SMEM, s, node_map, cache_map,
+                                     static_cast<const bf16*>(qkv), static_cast<bf16*>(y), a);
+}
+
+// Pipeline-wait limit of this file's kernels on the current device (0: the default).
+GPT_DEFINE_WAIT_LIMIT_SETTER(set_wait_limit_tree)
+
+}  // namespace gpt

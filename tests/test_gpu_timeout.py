@@ -102,3 +102,30 @@ def test_decode_step_wait_limit_gives_timeout_then_recovers():
         assert native.check_status(ws) == native.GPT_OK
         runs.append(logits)
     assert torch.equal(runs[0], runs[1])
+
+
+@pytest.mark.parametrize("N", [20, 64])
+def test_tree_attention_wait_limit_gives_timeout_then_recovers(short_waits, N):
+    """Clusters of CTAs: every CTA gives up, and none leaves before the others have read its part."""
+    native = short_waits
+    g = torch.Generator(device="cuda").manual_seed(73)
+    qkv = torch.randn((2, N, 3, 128), generator=g, device="cuda").to(torch.bfloat16)
+    kv = torch.randn((2, 700, 2, 128), generator=g, device="cuda").to(torch.bfloat16)
+    lens = torch.tensor([700, 300], dtype=torch.int32, device="cuda")
+    par = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(2, 1)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.tree_attention(qkv, kv, lens, par, 2, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_ERR_TIMEOUT
+    native.set_wait_limit_ns(0)
+    st.zero_()
+    y = native.tree_attention(qkv, kv, lens, par, 2, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_OK
+    for b in range(2):                                   # a chain: the tail of causal attention
+        n = int(lens[b])
+        x = torch.cat([kv[b, :n], qkv[b, :, 1:]]).float().view(n + N, 2, 2, 64)
+        q = qkv[b, :, 0].float().view(N, 2, 64).transpose(0, 1)
+        mask = torch.ones((N, n + N), dtype=torch.bool, device="cuda").tril(n)
+        ref = torch.nn.functional.scaled_dot_product_attention(q, x[:, 0].transpose(0, 1), x[:, 1].transpose(0, 1), attn_mask=mask)
+        assert float((y[b].float() - ref.transpose(0, 1).reshape(N, 128)).abs().max()) <= 2e-2
