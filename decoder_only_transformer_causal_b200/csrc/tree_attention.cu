@@ -8,6 +8,8 @@
 // softmax (running maximum, sum and weighted values, all fp32), and the parts are joined over distributed
 // shared memory in a fixed order, so the call needs no workspace and its results are reproducible.
 #include <math.h>
+#include <stdlib.h>
+#include <type_traits>
 
 #include "internal.h"
 #include "tree.cuh"
@@ -19,7 +21,8 @@ namespace {
 struct TreeArgs {
     const int* lengths;
     const int* parents;
-    int N, nh, hs, block_size, cluster;
+    int B, N, nh, hs, block_size, cluster;
+    int longest_first;   // CTAs take the sequences in the order of their lengths
     float scale_log2;   // log2(e) / sqrt(hs)
     int32_t* status;
 };
@@ -38,51 +41,52 @@ GPT_DEVINL float2 ld_cluster_f2(uint32_t cluster_addr) {
     return v;
 }
 
-GPT_DEVINL void st4(bf16* p, const float4& v) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-}
-GPT_DEVINL void st4(float* p, const float4& v) { *reinterpret_cast<float4*>(p) = v; }
-
-// Parts of a softmax over disjoint keys: weighted values o, {maximum (log2 units), sum}.  A part without
-// keys has a sum of 0 and its o is not looked at.
+// Parts of a softmax over disjoint keys: weighted values o (eight of a row), {maximum (log2 units), sum}.
+// A part without keys has a sum of 0 and its o is not looked at.
 struct Joined {
-    float M = -INFINITY, L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, L = 0.f, o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     GPT_DEVINL void see(const float2& ml) {
         if (ml.y != 0.f) M = fmaxf(M, ml.x);
     }
-    GPT_DEVINL float weight(const float2& ml) const { return ml.x == M ? 1.f : exp2_approx(ml.x - M); }
-    GPT_DEVINL void add(const float2& ml, const float4& v) {
-        const float w = weight(ml);
-        L = fmaf(w, ml.y, L);
-        o.x = fmaf(w, v.x, o.x), o.y = fmaf(w, v.y, o.y), o.z = fmaf(w, v.z, o.z), o.w = fmaf(w, v.w, o.w);
+    GPT_DEVINL void add(const float2& ml, const float4& v, const float4& w) {
+        const float f = ml.x == M ? 1.f : exp2_approx(ml.x - M);
+        L = fmaf(f, ml.y, L);
+        o[0] = fmaf(f, v.x, o[0]), o[1] = fmaf(f, v.y, o[1]), o[2] = fmaf(f, v.z, o[2]), o[3] = fmaf(f, v.w, o[3]);
+        o[4] = fmaf(f, w.x, o[4]), o[5] = fmaf(f, w.y, o[5]), o[6] = fmaf(f, w.z, o[6]), o[7] = fmaf(f, w.w, o[7]);
+    }
+    GPT_DEVINL void finish() {
+        const float inv = 1.f / L;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= inv;
     }
 };
 
 // The parts that the cluster's CTAs left at the same place of their shared memory (o [N][ld], ml [N]),
-// joined in the order of their ranks and written; each CTA takes a share of the rows' 16-byte pieces.
-// fix(i, d, v): what is added to a finished piece.
+// joined in the order of their ranks and written; each CTA takes a share of the rows' pieces of eight.
+// per: pieces of a row; finish(i, d, joined): the rows that are nodes.
 template <typename E, typename F>
 GPT_DEVINL void join_cluster(const float* o, int ld, const float2* ml, const unsigned long long* see, const TreeArgs& a,
-                             int rank, E* y, long long row_stride, F fix) {
-    const int per = a.hs / 4;
+                             int per, int rank, E* y, long long row_stride, F finish) {
     for (int it = rank * blockDim.x + threadIdx.x; it < a.N * per; it += a.cluster * blockDim.x) {
-        const int i = it / per, d = (it - i * per) * 4;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int i = it / per, d = (it - i * per) * 8;
+        Joined j;
         if (see[i]) {
-            Joined j;
             float2 part[8];
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                if (q < a.cluster) part[q] = ld_cluster_f2(map_to_rank(&ml[i], q)), j.see(part[q]);
+                if (q < a.cluster) part[q] = ld_cluster_f2(map_to_rank(&ml[i], q));
 #pragma unroll
             for (int q = 0; q < 8; ++q)
-                if (q < a.cluster && part[q].y != 0.f) j.add(part[q], ld_cluster_f4(map_to_rank(&o[i * ld + d], q)));
-            const float inv = 1.f / j.L;
-            v = make_float4(j.o.x * inv, j.o.y * inv, j.o.z * inv, j.o.w * inv);
-            fix(i, d, v);
+                if (q < a.cluster) j.see(part[q]);
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                if (q < a.cluster && part[q].y != 0.f) {
+                    const uint32_t at = map_to_rank(&o[i * ld + d], q);
+                    j.add(part[q], ld_cluster_f4(at), ld_cluster_f4(at + 16));
+                }
+            finish(i, d, j);
         }
-        st4(y + i * row_stride + d, v);
+        st8(y + i * row_stride + d, j.o);
     }
 }
 
@@ -147,7 +151,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
     const int pair = static_cast<int>(blockIdx.x) / a.cluster;
-    const int b = pair / a.nh, h = pair - b * a.nh;
+    int b = pair / a.nh;
+    const int h = pair - b * a.nh;
 
     if (threadIdx.x == 0) {
         uint64_t* bars = &T.q_full;
@@ -171,6 +176,22 @@ __global__ void __launch_bounds__(THREADS, 2)
     griddep_launch_dependents();
     griddep_wait();
 
+    if (a.longest_first) {
+        // the sequence whose length has place b among all (equal lengths in order of index)
+        const int t = threadIdx.x;
+        const int mine = t < a.B ? __ldcg(a.lengths + t) : 0;
+        int* all = reinterpret_cast<int*>(T.ml);
+        if (t < a.B) all[t] = mine;
+        __syncthreads();
+        if (t < a.B) {
+            int place = 0;
+            for (int j = 0; j < a.B; ++j) place += all[j] > mine || (all[j] == mine && j < t);
+            if (place == b) T.par[0] = t;
+        }
+        __syncthreads();
+        b = T.par[0];
+        __syncthreads();
+    }
     const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && threadIdx.x == 0 ? a.status : nullptr);
     const int n_cache = (len + KEYS - 1) / KEYS;   // tiles of the cache; tile n_cache is the nodes'
     const int n_steps = rank <= n_cache ? (n_cache - rank) / a.cluster + 1 : 0;
@@ -417,42 +438,64 @@ __global__ void __launch_bounds__(THREADS, 2)
     // The groups joined within the CTA, then the CTAs.
     const float* parts = reinterpret_cast<const float*>(sK);
     float* joined = reinterpret_cast<float*>(sK) + KEYS * LD;
-    for (int it = threadIdx.x; it < a.N * (HS / 4); it += THREADS) {
-        const int i = it / (HS / 4), d = it % (HS / 4) * 4;
+    const long long C = static_cast<long long>(a.nh) * HS;
+    bf16* out = y + static_cast<long long>(b) * a.N * C + h * HS;
+    const bool alone = a.cluster == 1;
+    unsigned long long bad = T.bad;
+    auto finish = [&](int i, int d, Joined& j) {
+        j.finish();
+        for (unsigned long long todo = bad & T.see[i]; todo; todo &= todo - 1) {
+            const bf16* w = qkv + (static_cast<long long>(b) * a.N + __ffsll(todo) - 1) * 3 * C + 2 * C + h * HS + d;
+            float f[8];
+            ld8(w, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!isfinite(f[e])) j.o[e] += f[e];
+        }
+    };
+    for (int it = threadIdx.x; it < a.N * (HS / 8); it += THREADS) {
+        const int i = it / (HS / 8), d = it % (HS / 8) * 8;
+        float2 ml[KEYS / R];
         Joined j;
 #pragma unroll
-        for (int g = 0; g < KEYS / R; ++g) j.see(T.ml[g * R + i]);
+        for (int g = 0; g < KEYS / R; ++g) ml[g] = T.ml[g * R + i], j.see(ml[g]);
 #pragma unroll
         for (int g = 0; g < KEYS / R; ++g)
-            if (T.ml[g * R + i].y != 0.f)
-                j.add(T.ml[g * R + i], *reinterpret_cast<const float4*>(parts + (g * R + i) * LD + d));
-        *reinterpret_cast<float4*>(joined + i * LD + d) = j.o;
-        if (d == 0) T.joined_ml[i] = make_float2(j.M, j.L);
+            if (ml[g].y != 0.f) {
+                const float4* o = reinterpret_cast<const float4*>(parts + (g * R + i) * LD + d);
+                j.add(ml[g], o[0], o[1]);
+            }
+        if (alone) {
+            if (T.see[i]) {
+                finish(i, d, j);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) j.o[e] = 0.f;
+            }
+            st8(out + i * C + d, j.o);
+        } else {
+            st8(joined + i * LD + d, j.o);
+            if (d == 0) T.joined_ml[i] = make_float2(j.M, j.L);
+        }
     }
-    cluster_sync();
-    const unsigned long long bad = static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&T.bad) + 1, n_cache % a.cluster))) << 32 |
-                                   ld_cluster_u32(map_to_rank(&T.bad, n_cache % a.cluster));
-    const long long C = static_cast<long long>(a.nh) * HS;
-    join_cluster(joined, LD, T.joined_ml, T.see, a, rank, y + static_cast<long long>(b) * a.N * C + h * HS, C,
-                 [&](int i, int d, float4& v) {
-                     for (unsigned long long todo = bad & T.see[i]; todo; todo &= todo - 1) {
-                         const bf16* w = qkv + (static_cast<long long>(b) * a.N + __ffsll(todo) - 1) * 3 * C + 2 * C + h * HS + d;
-                         float* x = &v.x;
-                         for (int e = 0; e < 4; ++e) {
-                             const float f = __bfloat162float(__ushort_as_bfloat16(__ldcg(reinterpret_cast<const unsigned short*>(w + e))));
-                             if (!isfinite(f)) x[e] += f;
-                         }
-                     }
-                 });
     if (threadIdx.x == 0 && *abort_flag) set_status(a.status, GPT_ERR_TIMEOUT);
+    if (alone) return;
+    __syncwarp();
+    cluster_sync();
+    const int holder = n_cache % a.cluster;   // of the nodes' tile
+    bad = static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&T.bad) + 1, holder))) << 32 |
+          ld_cluster_u32(map_to_rank(&T.bad, holder));
+    join_cluster(joined, LD, T.joined_ml, T.see, a, HS / 8, rank, out, C, finish);
     __syncwarp();
     cluster_sync();   // no CTA leaves while another reads its part
 }
 }  // namespace tc
 
 // ---------------------------------------------------------------- fp32, head size 8 to 128
-// The same split in CUDA cores: tiles of 64 keys in shared memory, a thread has NB / 8 nodes x 4 keys of
-// the scores and NB / 8 nodes x hs / 16 dimensions of the values.
+// The same split in CUDA cores: tiles of 64 keys in shared memory; of the scores a thread has NB / 8 nodes
+// x 4 keys, of the values NB / 8 nodes x 4 G dimensions (NB: the nodes rounded up to 8, 16, 32 or 64;
+// G = 2 above head size 64).  Products are packed pairs of fp32 FMAs.  The next tile's K travels while the
+// values are summed, its V while the scores are.
 namespace simt {
 constexpr int THREADS = 128;
 constexpr int KEYS = 64;
@@ -460,11 +503,17 @@ constexpr int KEYS = 64;
 GPT_DEVINL void cp_async16(void* dst, const void* src, int src_bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(src_bytes) : "memory");
 }
-GPT_DEVINL void cp_async_wait_all() { asm volatile("cp.async.commit_group;\n\tcp.async.wait_group 0;" ::: "memory"); }
+GPT_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int PENDING> GPT_DEVINL void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
 
 constexpr int smem_floats(int nb, int hs) { return (nb + 2 * KEYS) * (hs + 4) + nb * (KEYS + 4); }
 
-template <int NB>
+GPT_DEVINL void lds_pairs(const float* p, uint64_t (&v)[2]) {
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(p);
+    v[0] = w.x, v[1] = w.y;
+}
+
+template <int NB, int G>
 __global__ void __launch_bounds__(THREADS)
     tree_attention_f32(const float* __restrict__ qkv, const float* __restrict__ kv, float* __restrict__ y, const TreeArgs a) {
     constexpr int RN = NB / 8;
@@ -484,54 +533,76 @@ __global__ void __launch_bounds__(THREADS)
     const long long C = static_cast<long long>(a.nh) * hs;
     const float* node = qkv + static_cast<long long>(b) * N * 3 * C + h * hs;
     const float* cache = kv + static_cast<long long>(b) * a.block_size * 2 * C + h * hs;
+    // rows are copied by 2^row_shift threads each, 16 bytes per thread
+    int row_shift = 1;
+    while (4 << row_shift < hs) ++row_shift;
+    const int row0 = tid >> row_shift, col = (tid & ((1 << row_shift) - 1)) * 4, row_step = THREADS >> row_shift;
+    // `rows` rows at src (stride elements apart) to dst [total][ld], zeros behind them
+    auto copy_rows = [&](float* dst, const float* src, long long stride, int rows, int total) {
+        if (col < hs)
+            for (int i = row0; i < total; i += row_step)
+                cp_async16(dst + i * ld + col, i < rows ? src + i * stride + col : node, i < rows ? 16 : 0);
+        cp_async_commit();
+    };
     griddep_launch_dependents();
     griddep_wait();
+    copy_rows(sQ, node, 3 * C, N, NB);
     const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && tid == 0 ? a.status : nullptr);
     const int n_cache = (len + KEYS - 1) / KEYS;
-    const int per = hs / 4;
-    for (int it = tid; it < NB * per; it += THREADS) {
-        const int i = it / per, d = (it - i * per) * 4;
-        cp_async16(sQ + i * ld + d, node + (i < N ? i * 3 * C + d : 0), i < N ? 16 : 0);
-    }
+    auto copy_tile = [&](int t, int v) {
+        float* dst = v ? sV : sK;
+        if (t > n_cache) cp_async_commit();
+        else if (t == n_cache) copy_rows(dst, node + (1 + v) * C, 3 * C, N, KEYS);
+        else copy_rows(dst, cache + static_cast<long long>(t) * KEYS * 2 * C + v * C, 2 * C, len - t * KEYS, KEYS);
+    };
+    copy_tile(rank, 0);
+    copy_tile(rank, 1);
     load_tree(a, b, h == 0 && rank == 0, par, see);
 
-    float o[RN][8], m[RN], l[RN];
+    uint64_t o[RN][2 * G];
+    float m[RN], l[RN];
 #pragma unroll
     for (int i = 0; i < RN; ++i) {
         m[i] = -INFINITY, l[i] = 0.f;
 #pragma unroll
-        for (int d = 0; d < 8; ++d) o[i][d] = 0.f;
+        for (int d = 0; d < 2 * G; ++d) o[i][d] = 0;
     }
     for (int t = rank; t <= n_cache; t += a.cluster) {
         const bool nodes = t == n_cache;
         const int keys = nodes ? N : min(KEYS, len - t * KEYS);
-        __syncthreads();
-        for (int it = tid; it < KEYS * per; it += THREADS) {
-            const int k = it / per, d = (it - k * per) * 4;
-            const float* src = nodes ? node + k * 3 * C + C + d : cache + (static_cast<long long>(t) * KEYS + k) * 2 * C + d;
-            const bool in = k < keys;
-            cp_async16(sK + k * ld + d, in ? src : node, in ? 16 : 0);
-            cp_async16(sV + k * ld + d, in ? src + C : node, in ? 16 : 0);
-        }
-        cp_async_wait_all();
+        cp_async_wait<1>();   // this tile's K (and the queries); its V may still travel
         __syncthreads();
         float s[RN][4];
+        {
+            uint64_t acc[RN][4];
 #pragma unroll
-        for (int i = 0; i < RN; ++i)
+            for (int i = 0; i < RN; ++i)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) s[i][k] = 0.f;
-        for (int d = 0; d < hs; d += 4) {
-            float4 kk[4];
+                for (int k = 0; k < 4; ++k) acc[i][k] = 0;
+#pragma unroll 2
+            for (int d = 0; d < hs; d += 4) {
+                uint64_t kk[4][2];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) kk[k] = *reinterpret_cast<const float4*>(sK + (tx + 16 * k) * ld + d);
+                for (int k = 0; k < 4; ++k) lds_pairs(sK + (tx + 16 * k) * ld + d, kk[k]);
 #pragma unroll
-            for (int i = 0; i < RN; ++i) {
-                const float4 q = *reinterpret_cast<const float4*>(sQ + (ty * RN + i) * ld + d);
+                for (int i = 0; i < RN; ++i) {
+                    uint64_t q[2];
+                    lds_pairs(sQ + (ty * RN + i) * ld + d, q);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    s[i][k] = fmaf(q.x, kk[k].x, fmaf(q.y, kk[k].y, fmaf(q.z, kk[k].z, fmaf(q.w, kk[k].w, s[i][k]))));
+                    for (int k = 0; k < 4; ++k) acc[i][k] = f2_fma(q[1], kk[k][1], f2_fma(q[0], kk[k][0], acc[i][k]));
+                }
             }
+#pragma unroll
+            for (int i = 0; i < RN; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float lo, hi;
+                    f2_unpack(acc[i][k], lo, hi);
+                    s[i][k] = lo + hi;
+                }
         }
+        __syncthreads();
+        copy_tile(t + a.cluster, 0);
 #pragma unroll
         for (int i = 0; i < RN; ++i) {
             const unsigned long long mine = see[ty * RN + i];
@@ -547,12 +618,12 @@ __global__ void __launch_bounds__(THREADS)
             for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
             mx = fmaxf(mx, m[i]);
             const float off = mx == -INFINITY ? 0.f : mx;
-            const float alpha = m[i] == mx ? 1.f : exp2f(m[i] - off);
+            const float alpha = m[i] == mx ? 1.f : exp2_approx(m[i] - off);
             m[i] = mx;
             float sum = 0.f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const float p = exp2f(s[i][k] - off);
+                const float p = exp2_approx(s[i][k] - off);
                 sP[(ty * RN + i) * (KEYS + 4) + tx + 16 * k] = p;
                 sum += p;
             }
@@ -560,52 +631,82 @@ __global__ void __launch_bounds__(THREADS)
             for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
             l[i] = l[i] * alpha + sum;
 #pragma unroll
-            for (int d = 0; d < 8; ++d) o[i][d] *= alpha;
+            for (int d = 0; d < 2 * G; ++d) o[i][d] = f2_mul(o[i][d], f2_pack(alpha, alpha));
         }
-        __syncwarp();   // a node's weights are written and read by the same half warp
-        for (int k = 0; k < KEYS; k += 4) {
-            float4 p[RN];
+        cp_async_wait<1>();   // this tile's V
+        __syncthreads();
+        auto sum_values = [&](auto is_nodes) {
+            unsigned long long mine[RN];
+            if (is_nodes) {
 #pragma unroll
-            for (int i = 0; i < RN; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * RN + i) * (KEYS + 4) + k);
+                for (int i = 0; i < RN; ++i) mine[i] = see[ty * RN + i];
+            }
+#pragma unroll 1
+            for (int k = 0; k < keys; k += 4) {   // (weights behind the last key are 0, V rows zeros)
+                float4 p[RN];
 #pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                float4 v[2];
+                for (int i = 0; i < RN; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * RN + i) * (KEYS + 4) + k);
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
-                    v[g] = tx * 4 + 64 * g < hs ? *reinterpret_cast<const float4*>(sV + (k + x) * ld + tx * 4 + 64 * g)
-                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x = 0; x < 4; ++x) {
+                    uint64_t v[G][2];
 #pragma unroll
-                for (int i = 0; i < RN; ++i) {
-                    // another branch's value may be NaN: it is not even multiplied by 0
-                    if (nodes && !((see[ty * RN + i] >> (k + x)) & 1)) continue;
-                    const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+                    for (int g = 0; g < G; ++g) {
+                        v[g][0] = v[g][1] = 0;
+                        if (tx * 4 + 64 * g < hs) lds_pairs(sV + (k + x) * ld + tx * 4 + 64 * g, v[g]);
+                    }
 #pragma unroll
-                    for (int g = 0; g < 2; ++g) {
-                        o[i][4 * g] = fmaf(w, v[g].x, o[i][4 * g]);
-                        o[i][4 * g + 1] = fmaf(w, v[g].y, o[i][4 * g + 1]);
-                        o[i][4 * g + 2] = fmaf(w, v[g].z, o[i][4 * g + 2]);
-                        o[i][4 * g + 3] = fmaf(w, v[g].w, o[i][4 * g + 3]);
+                    for (int i = 0; i < RN; ++i) {
+                        // another branch's value may be NaN: it is not even multiplied by 0
+                        if (is_nodes && !((mine[i] >> (k + x)) & 1)) continue;
+                        const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
+                        const uint64_t ww = f2_pack(w, w);
+#pragma unroll
+                        for (int g = 0; g < G; ++g) {
+                            o[i][2 * g] = f2_fma(ww, v[g][0], o[i][2 * g]);
+                            o[i][2 * g + 1] = f2_fma(ww, v[g][1], o[i][2 * g + 1]);
+                        }
                     }
                 }
             }
-        }
+        };
+        if (nodes) sum_values(std::true_type());
+        else sum_values(std::false_type());
+        __syncthreads();
+        copy_tile(t + a.cluster, 1);
     }
-    cp_async_wait_all();
+    cp_async_wait<0>();
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < RN; ++i) {
 #pragma unroll
-        for (int g = 0; g < 2; ++g)
+        for (int g = 0; g < G; ++g)
             if (tx * 4 + 64 * g < hs)
-                *reinterpret_cast<float4*>(sK + (ty * RN + i) * ld + tx * 4 + 64 * g) =
-                    make_float4(o[i][4 * g], o[i][4 * g + 1], o[i][4 * g + 2], o[i][4 * g + 3]);
+                *reinterpret_cast<ulonglong2*>(sK + (ty * RN + i) * ld + tx * 4 + 64 * g) = make_ulonglong2(o[i][2 * g], o[i][2 * g + 1]);
         if (tx == 0) ml[ty * RN + i] = make_float2(m[i], l[i]);
     }
     __syncthreads();
     cluster_sync();
-    join_cluster(sK, ld, ml, see, a, rank, y + static_cast<long long>(b) * N * C + h * hs, C, [](int, int, float4&) {});
+    join_cluster(sK, ld, ml, see, a, hs / 8, rank, y + static_cast<long long>(b) * N * C + h * hs, C,
+                 [](int, int, Joined& j) { j.finish(); });
     __syncwarp();
     cluster_sync();
+}
+
+template <int NB, int G>
+int launch(const void* qkv, const void* kv, void* y, const TreeArgs& a, unsigned ctas, cudaStream_t s) {
+    static size_t opted[kMaxDevices] = {};
+    const size_t smem = sizeof(float) * smem_floats(NB, a.hs);
+    const int rc = opt_in_smem(reinterpret_cast<const void*>(tree_attention_f32<NB, G>), smem, opted);
+    if (rc) return rc;
+    return launch_overlapped_cluster(tree_attention_f32<NB, G>, a.cluster, dim3(ctas), dim3(THREADS), smem, s,
+                                     static_cast<const float*>(qkv), static_cast<const float*>(kv), static_cast<float*>(y), a);
+}
+template <int G>
+int launch(const void* qkv, const void* kv, void* y, const TreeArgs& a, unsigned ctas, cudaStream_t s) {
+    if (a.N <= 8) return launch<8, G>(qkv, kv, y, a, ctas, s);
+    if (a.N <= 16) return launch<16, G>(qkv, kv, y, a, ctas, s);
+    if (a.N <= 32) return launch<32, G>(qkv, kv, y, a, ctas, s);
+    return launch<64, G>(qkv, kv, y, a, ctas, s);
 }
 }  // namespace simt
 
@@ -616,6 +717,7 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
     TreeArgs a = {};
     a.lengths = lengths;
     a.parents = parents;
+    a.B = B;
     a.N = N;
     a.nh = nh;
     a.hs = hs;
@@ -626,20 +728,14 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
     const long long pairs = static_cast<long long>(B) * nh;
     const int tiles = (block_size - 1) / (f32 ? simt::KEYS : tc::KEYS) + 2;
     a.cluster = 1;
-    while (a.cluster < 8 && pairs * a.cluster < 148 * 8 && a.cluster < tiles) a.cluster *= 2;
+    const long long slots = 148 * (f32 ? 5 : 2);   // CTAs that run at a time
+    while (a.cluster < 8 && pairs * a.cluster * 2 <= slots && a.cluster < tiles) a.cluster *= 2;
+    if (getenv("TREE_CL")) a.cluster = atoi(getenv("TREE_CL"));
+    // more CTAs than run at a time: those with the most work start first
+    a.longest_first = !f32 && B > 1 && B <= tc::THREADS && pairs * a.cluster > slots;
     const dim3 grid(static_cast<unsigned>(pairs * a.cluster));
+    if (f32) return hs <= 64 ? simt::launch<1>(qkv, kv, y, a, grid.x, s) : simt::launch<2>(qkv, kv, y, a, grid.x, s);
     int rc;
-    if (f32) {
-        const size_t smem = sizeof(float) * simt::smem_floats(N <= 16 ? 16 : 64, hs);
-        static size_t opted16[kMaxDevices] = {}, opted64[kMaxDevices] = {};
-        auto kern = N <= 16 ? simt::tree_attention_f32<16> : simt::tree_attention_f32<64>;
-        rc = N <= 16 ? opt_in_smem(reinterpret_cast<const void*>(kern), smem, opted16)
-                     : opt_in_smem(reinterpret_cast<const void*>(kern), smem, opted64);
-        if (rc) return rc;
-        return launch_overlapped_cluster(kern, a.cluster, grid, dim3(simt::THREADS), smem, s,
-                                         static_cast<const float*>(qkv), static_cast<const float*>(kv),
-                                         static_cast<float*>(y), a);
-    }
     // {hs, heads of q, k, v (nodes) or k, v (cache), rows, sequences}
     const uint64_t C2 = static_cast<uint64_t>(nh) * hs * 2;
     const uint64_t node_dims[4] = {64, static_cast<uint64_t>(3) * nh, static_cast<uint64_t>(N), static_cast<uint64_t>(B)};

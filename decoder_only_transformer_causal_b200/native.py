@@ -491,26 +491,70 @@ def generate(cfg: GPTConfig, weights: torch.Tensor, idx: torch.Tensor, max_new_t
 
 
 # ---------------------------------------------------------------- drafted trees
-def _arg(name: str, t: torch.Tensor, dtype, shape, like: torch.Tensor) -> int:
-    """The device pointer of a contiguous tensor of the given dtype and shape on like's device."""
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape):
+# These calls come once per layer or per token, and their kernels take a few microseconds: the checks
+# below are written to cost little on the path where nothing is wrong.
+_STORED = {torch.bfloat16: GPT_DTYPE_BF16, torch.float32: GPT_DTYPE_F32}
+
+
+def _arg(name: str, t: torch.Tensor, dtype, shape, device) -> int:
+    """The device pointer of a contiguous tensor of the given dtype, shape and device."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    if t.dtype is not dtype or t.shape != shape:
         raise ValueError(f"{name} must be {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, expected {like.device}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _status_arg(status, device):
+    return None if status is None else _arg("status", status, torch.int32, status.shape, device)
+
+
+def _buffer(name: str, t: torch.Tensor, nbytes: int, device) -> int:
+    """The pointer of a contiguous buffer of at least nbytes, whatever its dtype and shape."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    if t.numel() * t.element_size() < nbytes:
+        raise ValueError(f"{name} holds {t.numel() * t.element_size()} bytes, {nbytes} are needed")
     return t.data_ptr()
 
 
-def _on(t: torch.Tensor):
-    """Makes t's device current (the call's stream and launches belong to it)."""
+def _cuda_index(t: torch.Tensor) -> int:
     if not t.is_cuda:
         raise ValueError(f"expected CUDA tensors, got one on {t.device}")
-    return torch.cuda.device(t.device)
+    return t.get_device()
 
 
-def _status_arg(status, like):
-    return None if status is None else _arg("status", status, torch.int32, status.shape, like)
+def _stream_of(index: int, stream) -> int | None:
+    """The stream's handle; by default the current stream of device `index`."""
+    return torch._C._cuda_getCurrentRawStream(index) or None if stream is None else _stream(stream)
+
+
+def _launch(where: str, index: int, *args) -> None:
+    """LIB.where(*args) with device `index` current."""
+    if index == torch.cuda.current_device():
+        rc = getattr(LIB, where)(*args)
+    else:
+        with torch.cuda.device(index):
+            rc = getattr(LIB, where)(*args)
+    if rc != GPT_OK:
+        raise GPTError(rc, where)
+
+
+def _cfg_ref(cfg: GPTConfig):
+    """byref of cfg's C form, made once per (frozen) configuration."""
+    kept = cfg.__dict__.get("_cref")
+    if kept is None:
+        kept = ctypes.byref(cfg.c())
+        cfg.__dict__["_cref"] = kept
+    return kept
+
+
+def _kv_bytes(cfg: GPTConfig, B: int) -> int:
+    return cfg.n_layer * B * cfg.block_size * 2 * cfg.n_embd * cfg.torch_dtype.itemsize
 
 
 def kv_layers(cfg: GPTConfig, kv_cache: torch.Tensor, B: int) -> torch.Tensor:
@@ -529,19 +573,19 @@ def tree_attention(qkv: torch.Tensor, kv: torch.Tensor, lengths: torch.Tensor, p
                    y: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """gpt_tree_attention: qkv [B, N, 3, C], one layer's cache kv [B, block_size, 2, C], lengths int32 [B],
     parents int32 [B, N] (-1 root, -2 no node); returns y [B, N, C]."""
-    if qkv.dim() != 4 or qkv.shape[2] != 3 or kv.dim() != 4:
-        raise ValueError("qkv must be [B, N, 3, C] and kv [B, block_size, 2, C]")
+    if qkv.dim() != 4 or qkv.shape[2] != 3 or kv.dim() != 4 or qkv.dtype not in _STORED:
+        raise ValueError("qkv must be a bfloat16 or float32 [B, N, 3, C] tensor and kv [B, block_size, 2, C]")
     B, N, _, C = qkv.shape
+    cap = kv.shape[1]
     if n_head < 1 or C % n_head:
         raise ValueError("C must be a multiple of n_head")
-    with _on(qkv):
-        if y is None:
-            y = torch.empty((B, N, C), dtype=qkv.dtype, device=qkv.device)
-        _check(LIB.gpt_tree_attention(
-            _arg("qkv", qkv, qkv.dtype, (B, N, 3, C), qkv), _arg("kv", kv, qkv.dtype, (B, kv.shape[1], 2, C), qkv),
-            _arg("lengths", lengths, torch.int32, (B,), qkv), _arg("parents", parents, torch.int32, (B, N), qkv),
-            _arg("y", y, qkv.dtype, (B, N, C), qkv), B, N, n_head, C // n_head, kv.shape[1], _dt(qkv),
-            _status_arg(status, qkv), _stream(stream)), "gpt_tree_attention")
+    index, dt, dev = _cuda_index(qkv), qkv.dtype, qkv.device
+    if y is None:
+        y = qkv.new_empty((B, N, C))
+    _launch("gpt_tree_attention", index, _arg("qkv", qkv, dt, (B, N, 3, C), dev),
+            _arg("kv", kv, dt, (B, cap, 2, C), dev), _arg("lengths", lengths, torch.int32, (B,), dev),
+            _arg("parents", parents, torch.int32, (B, N), dev), _arg("y", y, dt, (B, N, C), dev), B, N, n_head,
+            C // n_head, cap, _STORED[dt], _status_arg(status, dev), _stream_of(index, stream))
     return y
 
 
@@ -551,17 +595,15 @@ def tree_step(cfg: GPTConfig, weights: torch.Tensor, tok: torch.Tensor, parents:
     """gpt_tree_step: tok int64 [B, N], parents int32 [B, N], lengths int32 [B]; fills tree_qkv
     (alloc_tree_qkv) and returns the nodes' logits [B, N, V] in cfg's dtype."""
     B, N = tok.shape
-    with _on(tok):
-        if logits is None:
-            logits = torch.empty((B, N, cfg.vocab_size), dtype=cfg.torch_dtype, device=tok.device)
-        if kv_cache.numel() * kv_cache.element_size() < kv_cache_bytes(cfg, B):
-            raise ValueError("kv_cache is smaller than gpt_kv_cache_bytes")
-        _check(LIB.gpt_tree_step(
-            ctypes.byref(cfg.c()), _ptr(weights), _arg("tok", tok, torch.int64, (B, N), tok),
-            _arg("parents", parents, torch.int32, (B, N), tok), _arg("lengths", lengths, torch.int32, (B,), tok), B, N,
-            _ptr(kv_cache), _arg("tree_qkv", tree_qkv, cfg.torch_dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), tok),
-            _arg("logits", logits, cfg.torch_dtype, (B, N, cfg.vocab_size), tok), _ptr(workspace), workspace.numel(),
-            _stream(stream), GPT_FLAG_SYNC_CHECK if sync_check else 0), "gpt_tree_step")
+    index, dt, dev = _cuda_index(tok), cfg.torch_dtype, tok.device
+    if logits is None:
+        logits = torch.empty((B, N, cfg.vocab_size), dtype=dt, device=dev)
+    _launch("gpt_tree_step", index, _cfg_ref(cfg), _ptr(weights), _arg("tok", tok, torch.int64, (B, N), dev),
+            _arg("parents", parents, torch.int32, (B, N), dev), _arg("lengths", lengths, torch.int32, (B,), dev), B, N,
+            _buffer("kv_cache", kv_cache, _kv_bytes(cfg, B), dev),
+            _arg("tree_qkv", tree_qkv, dt, (cfg.n_layer, B, N, 3, cfg.n_embd), dev),
+            _arg("logits", logits, dt, (B, N, cfg.vocab_size), dev), _buffer("workspace", workspace, 0, dev),
+            workspace.numel(), _stream_of(index, stream), GPT_FLAG_SYNC_CHECK if sync_check else 0)
     return logits
 
 
@@ -578,25 +620,18 @@ def tree_accept(cfg: GPTConfig, parents: torch.Tensor, tok: torch.Tensor, chosen
     """gpt_tree_accept: keeps the drafted path that `chosen` confirms and copies its k, v into the cache.
     out: buffers to write (out.lengths may be `lengths` itself)."""
     B, N = parents.shape
-    dev = parents.device
-    with _on(parents):
-        if out is None:
-            out = TreeAccept(torch.empty((B, N), dtype=torch.int32, device=dev),
-                             torch.empty(B, dtype=torch.int32, device=dev),
-                             torch.empty(B, dtype=torch.int64, device=dev),
-                             torch.empty(B, dtype=torch.int32, device=dev))
-        if kv_cache.numel() * kv_cache.element_size() < kv_cache_bytes(cfg, B):
-            raise ValueError("kv_cache is smaller than gpt_kv_cache_bytes")
-        _check(LIB.gpt_tree_accept(
-            ctypes.byref(cfg.c()), _arg("parents", parents, torch.int32, (B, N), parents),
-            _arg("tok", tok, torch.int64, (B, N), parents), _arg("chosen", chosen, torch.int64, (B, N), parents),
-            _arg("lengths", lengths, torch.int32, (B,), parents), B, N,
-            _arg("tree_qkv", tree_qkv, cfg.torch_dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), parents), _ptr(kv_cache),
-            _arg("path", out.path, torch.int32, (B, N), parents),
-            _arg("n_accepted", out.n_accepted, torch.int32, (B,), parents),
-            _arg("next_token", out.next_token, torch.int64, (B,), parents),
-            _arg("lengths_out", out.lengths, torch.int32, (B,), parents), _status_arg(status, parents),
-            _stream(stream)), "gpt_tree_accept")
+    index, dev, i32 = _cuda_index(parents), parents.device, torch.int32
+    if out is None:
+        n, new = parents.new_empty((2, B)).unbind(0)
+        out = TreeAccept(parents.new_empty((B, N)), n, torch.empty(B, dtype=torch.int64, device=dev), new)
+    _launch("gpt_tree_accept", index, _cfg_ref(cfg), _arg("parents", parents, i32, (B, N), dev),
+            _arg("tok", tok, torch.int64, (B, N), dev), _arg("chosen", chosen, torch.int64, (B, N), dev),
+            _arg("lengths", lengths, i32, (B,), dev), B, N,
+            _arg("tree_qkv", tree_qkv, cfg.torch_dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), dev),
+            _buffer("kv_cache", kv_cache, _kv_bytes(cfg, B), dev), _arg("path", out.path, i32, (B, N), dev),
+            _arg("n_accepted", out.n_accepted, i32, (B,), dev),
+            _arg("next_token", out.next_token, torch.int64, (B,), dev),
+            _arg("lengths_out", out.lengths, i32, (B,), dev), _status_arg(status, dev), _stream_of(index, stream))
     return out
 
 
@@ -611,15 +646,17 @@ class TokenLogprobs(NamedTuple):
 
 def _rows(name: str, t: torch.Tensor, like: torch.Tensor):
     """(pointer, row stride) of a [rows, V] tensor whose rows may lie apart."""
-    if t.dim() != 2 or t.dtype not in (torch.bfloat16, torch.float32):
+    if t.dim() != 2 or t.dtype not in _STORED:
         raise ValueError(f"{name} must be a bfloat16 or float32 [rows, V] tensor")
-    if t.shape != like.shape or t.dtype != like.dtype or t.device != like.device:
+    if t is not like and (t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the logits' shape, dtype and device")
     rows, V = t.shape
-    if V > 1 and t.stride(1) != 1:
+    ld, one = t.stride()
+    if V > 1 and one != 1:
         raise ValueError(f"{name}: the entries of a row must be contiguous")
-    ld = t.stride(0) if rows > 1 else max(V, 1)
-    if ld < V:
+    if rows <= 1:
+        ld = max(V, 1)
+    elif ld < V:
         raise ValueError(f"{name}: rows overlap")
     return t.data_ptr() or None, ld
 
@@ -630,22 +667,22 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: 
     padded vocabulary), tokens int64 [rows] (-1: none).  out: buffers to write."""
     ptr, ld = _rows("logits", logits, logits)
     rows, V = logits.shape
-    with _on(logits):
-        if out is None:
-            def buf(*shape, dtype=torch.float32):
-                return torch.empty(shape, dtype=dtype, device=logits.device)
-            out = TokenLogprobs(buf(rows) if tokens is not None else None, buf(rows), buf(rows),
-                                buf(rows, k, dtype=torch.int64) if k else None, buf(rows, k) if k else None)
-
-        def opt(name, t, dtype, shape):
-            return None if t is None else _arg(name, t, dtype, shape, logits)
-        if rows:
-            _check(LIB.gpt_token_logprobs(
-                ptr, ld, opt("tokens", tokens, torch.int64, (rows,)), rows, V, _dt(logits), float(temperature),
-                opt("logp", out.logp, torch.float32, (rows,)), opt("entropy", out.entropy, torch.float32, (rows,)),
-                opt("lse", out.lse, torch.float32, (rows,)), int(k), opt("top_ids", out.top_ids, torch.int64, (rows, k)),
-                opt("top_logp", out.top_logp, torch.float32, (rows, k)), _status_arg(status, logits), _stream(stream)),
-                "gpt_token_logprobs")
+    index, dev, f32 = _cuda_index(logits), logits.device, torch.float32
+    if out is None:
+        logp, entropy, lse = torch.empty((3, rows), dtype=f32, device=dev).unbind(0)
+        out = TokenLogprobs(logp if tokens is not None else None, entropy, lse,
+                            torch.empty((rows, k), dtype=torch.int64, device=dev) if k else None,
+                            torch.empty((rows, k), dtype=f32, device=dev) if k else None)
+    if rows:
+        _launch("gpt_token_logprobs", index, ptr, ld,
+                None if tokens is None else _arg("tokens", tokens, torch.int64, (rows,), dev), rows, V,
+                _STORED[logits.dtype], float(temperature),
+                None if out.logp is None else _arg("logp", out.logp, f32, (rows,), dev),
+                None if out.entropy is None else _arg("entropy", out.entropy, f32, (rows,), dev),
+                None if out.lse is None else _arg("lse", out.lse, f32, (rows,), dev), int(k),
+                None if out.top_ids is None else _arg("top_ids", out.top_ids, torch.int64, (rows, k), dev),
+                None if out.top_logp is None else _arg("top_logp", out.top_logp, f32, (rows, k), dev),
+                _status_arg(status, dev), _stream_of(index, stream))
     return out
 
 
@@ -657,19 +694,18 @@ def token_logprobs_backward(logits: torch.Tensor, tokens: torch.Tensor | None, l
     logits' dtype (into `dlogits` when given, which may be the logits themselves)."""
     ptr, ld = _rows("logits", logits, logits)
     rows, V = logits.shape
-    with _on(logits):
-        if dlogits is None:
-            dlogits = torch.empty((rows, V), dtype=logits.dtype, device=logits.device)
-        dptr, ldd = _rows("dlogits", dlogits, logits)
-
-        def opt(name, t, dtype):
-            return None if t is None else _arg(name, t, dtype, (rows,), logits)
-        if rows:
-            _check(LIB.gpt_token_logprobs_backward(
-                ptr, ld, opt("tokens", tokens, torch.int64), rows, V, _dt(logits), float(temperature),
-                opt("lse", lse, torch.float32), opt("entropy", entropy, torch.float32),
-                opt("dlogp", dlogp, torch.float32), opt("dentropy", dentropy, torch.float32), dptr, ldd,
-                _status_arg(status, logits), _stream(stream)), "gpt_token_logprobs_backward")
+    index, dev, f32 = _cuda_index(logits), logits.device, torch.float32
+    if dlogits is None:
+        dlogits = logits.new_empty((rows, V))
+    dptr, ldd = _rows("dlogits", dlogits, logits)
+    if rows:
+        _launch("gpt_token_logprobs_backward", index, ptr, ld,
+                None if tokens is None else _arg("tokens", tokens, torch.int64, (rows,), dev), rows, V,
+                _STORED[logits.dtype], float(temperature), _arg("lse", lse, f32, (rows,), dev),
+                None if entropy is None else _arg("entropy", entropy, f32, (rows,), dev),
+                None if dlogp is None else _arg("dlogp", dlogp, f32, (rows,), dev),
+                None if dentropy is None else _arg("dentropy", dentropy, f32, (rows,), dev), dptr, ldd,
+                _status_arg(status, dev), _stream_of(index, stream))
     return dlogits
 
 
