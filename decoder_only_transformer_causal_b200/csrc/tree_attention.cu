@@ -8,7 +8,6 @@
 // softmax (running maximum, sum and weighted values, all fp32), and the parts are joined over distributed
 // shared memory in a fixed order, so the call needs no workspace and its results are reproducible.
 #include <math.h>
-#include <stdlib.h>
 #include <type_traits>
 
 #include "internal.h"
@@ -41,6 +40,20 @@ GPT_DEVINL float2 ld_cluster_f2(uint32_t cluster_addr) {
     return v;
 }
 
+// named_barrier that returns whether any of its threads passed true.
+GPT_DEVINL bool named_barrier_or(int id, int threads, bool v) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 q, %3, 0;\n\t"
+        "barrier.cta.red.or.pred p, %1, %2, q;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return r != 0;
+}
+
 // Parts of a softmax over disjoint keys: weighted values o (eight of a row), {maximum (log2 units), sum}.
 // A part without keys has a sum of 0 and its o is not looked at.
 struct Joined {
@@ -58,6 +71,17 @@ struct Joined {
         const float inv = 1.f / L;
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] *= inv;
+    }
+    // ... and adds the values that are not finite of the rows in `from` (at v, stride elements apart)
+    GPT_DEVINL void finish(unsigned long long from, const bf16* v, long long stride) {
+        finish();
+        for (; from; from &= from - 1) {
+            float f[8];
+            ld8(v + (__ffsll(from) - 1) * stride, f);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (!isfinite(f[e])) o[e] += f[e];
+        }
     }
 };
 
@@ -111,52 +135,97 @@ GPT_DEVINL void load_tree(const TreeArgs& a, int b, bool report, int* par, unsig
 //     one chain of products accumulates every group's share, joined at the end.
 // The repeated rows cost tensor time (2 cycles per key of the 11 that its bytes take at this GPU's copy
 // rate) and save the transposes and shuffles that splitting the keys over lanes would take.
-// Warp 0 issues the loads, warp 1 the products, warps 2-5 the softmax, two CTAs share an SM.
+//
+// The nodes' own keys lie in the last R rows of the last tile, behind the cache's rest if that leaves room.
+//
+// Warp 0 issues the loads, warp 1 the products, warps 2-5 the softmax; two CTAs share an SM.  With more
+// pairs of sequence and head than run at a time the CTAs are persistent, so that a pair's first loads and
+// products run under the join of the one before, and take the pairs longest first, every other round in
+// reverse (sequences of up to THREADS; beyond that in the order given).
 //
 // The product multiplies masked values by 0, so values that must not be seen are made harmless in shared
-// memory: V rows behind the sequence's end are cleared; in the nodes' tile, rows of absent nodes are
-// cleared and values that are not finite are replaced by 0 and added at the end to the rows that see them.
+// memory: V rows between the cache's end and the nodes, and of absent nodes, are cleared; values of nodes
+// that are not finite are replaced by 0 and added at the end to the rows that see them.
 namespace tc {
 constexpr int HS = 64;
 constexpr int KEYS = 128;
-constexpr int BOX = 32;                       // rows per load of the nodes' q, k, v
+constexpr int BOX = 32;                       // rows per load of the nodes' q, k, v and of the cache's rest
+constexpr int BOX_BYTES = BOX * HS * 2;
 constexpr int THREADS = 192;
 constexpr int TILE = KEYS * HS * 2;           // 16 KB
-constexpr int LD = HS + 4;                    // floats per row of an exported part
+constexpr int HALF = HS / 2, HALF_LD = HALF + 4;   // the groups' parts are joined half a row at a time
+constexpr int LD = HS + 4;                    // floats per row of the CTA's part
 constexpr int STAGES = 2;
 constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_P = 128, COL_O = 192;
 constexpr float kRescaleThreshold = 8.f;      // as in the causal kernel: P stays below 2^8
 
 struct Tail {
-    uint64_t q_full, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full, s_free, p_full, o_done, drain;
+    uint64_t q_full, q_empty, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full, s_free, p_full, o_done, drain;
     unsigned long long see[kMaxNodes], bad;   // bad: node rows of V with values that are not finite
     float2 ml[KEYS], joined_ml[kMaxNodes];
     int par[kMaxNodes];
+    int lengths[THREADS];                     // with longest_first: in the order of the pairs,
+    short order[THREADS];                     // and the sequences they belong to
     uint32_t tmem;
     int abort;
 };
-constexpr int SMEM = (1 + 2 * STAGES) * TILE + static_cast<int>(sizeof(Tail)) + 1024;
+constexpr int SMEM = (1 + 2 * STAGES) * TILE + KEYS * HALF_LD * 4 + static_cast<int>(sizeof(Tail)) + 1024;
+
+// One sequence and head, as one CTA of its cluster sees it.
+struct Work {
+    int b, h, len, n_cache, rest, n_tiles, n_steps;   // rest: keys of the cache in the last tile
+    GPT_DEVINL bool last(int j) const { return j == n_steps - 1 && has_nodes; }
+    bool has_nodes;
+};
+
+template <int R>
+GPT_DEVINL Work work_of(int pair, const TreeArgs& a, const Tail& T, int rank, int32_t* status) {
+    Work w;
+    w.b = pair / a.nh;
+    w.h = pair - w.b * a.nh;
+    int len;
+    if (a.longest_first) {
+        len = T.lengths[w.b];
+        w.b = T.order[w.b];
+    } else {
+        len = __ldcg(a.lengths + w.b);
+    }
+    w.len = clamp_length(len, a.block_size, w.h == 0 ? status : nullptr);
+    w.n_cache = w.len / KEYS;               // tiles of the cache alone
+    w.rest = w.len - w.n_cache * KEYS;
+    if (w.rest > KEYS - R) ++w.n_cache, w.rest = 0;
+    w.n_tiles = w.n_cache + 1;
+    w.n_steps = rank < w.n_tiles ? (w.n_tiles - 1 - rank) / a.cluster + 1 : 0;
+    w.has_nodes = w.n_cache % a.cluster == rank;
+    return w;
+}
 
 template <int R>
 __global__ void __launch_bounds__(THREADS, 2)
     tree_attention_tc(const __grid_constant__ CUtensorMap tmNode, const __grid_constant__ CUtensorMap tmCache,
-                      const bf16* __restrict__ qkv, bf16* __restrict__ y, const TreeArgs a) {
+                      const __grid_constant__ CUtensorMap tmRest, const bf16* __restrict__ qkv, bf16* __restrict__ y,
+                      const TreeArgs a) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sQ = smem;
     uint8_t* sK = smem + TILE;
     uint8_t* sV = sK + STAGES * TILE;
-    Tail& T = *reinterpret_cast<Tail*>(sV + STAGES * TILE);
+    float* sPart = reinterpret_cast<float*>(sV + STAGES * TILE);
+    float* joined = reinterpret_cast<float*>(sK) + KEYS * LD;   // in a cluster, which has one pair
+    Tail& T = *reinterpret_cast<Tail*>(sPart + KEYS * HALF_LD);
     volatile int* abort_flag = &T.abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = static_cast<int>(cluster_ctarank());
-    const int pair = static_cast<int>(blockIdx.x) / a.cluster;
-    int b = pair / a.nh;
-    const int h = pair - b * a.nh;
+    // pairs: this CTA's (its cluster's) first, then one per round of the grid, every other round in reverse
+    const int n_pairs = a.B * a.nh, pair_stride = static_cast<int>(gridDim.x) / a.cluster;
+    const int pair0 = static_cast<int>(blockIdx.x) / a.cluster;
+    auto pair_at = [&](int round) {
+        return round * pair_stride + ((round & 1) ? pair_stride - 1 - pair0 : pair0);
+    };
 
     if (threadIdx.x == 0) {
         uint64_t* bars = &T.q_full;
-        constexpr int n_bars = 1 + 4 * STAGES + 5;
+        constexpr int n_bars = 2 + 4 * STAGES + 5;
         for (int i = 0; i < n_bars; ++i) mbar_init(&bars[i], (&bars[i] == &T.s_free || &bars[i] == &T.p_full) ? 128u : 1u);
         T.abort = 0;
         T.bad = 0;
@@ -164,194 +233,227 @@ __global__ void __launch_bounds__(THREADS, 2)
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         tma_prefetch_desc(&tmNode);
         tma_prefetch_desc(&tmCache);
+        tma_prefetch_desc(&tmRest);
     }
     if (warp == 1) {
         tmem_alloc(&T.tmem, TMEM_COLS);
         tmem_relinquish();
     }
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    const uint32_t tmem = T.tmem;
     griddep_launch_dependents();
     griddep_wait();
-
-    if (a.longest_first) {
-        // the sequence whose length has place b among all (equal lengths in order of index)
+    if (a.longest_first) {   // the sequences in the order of their lengths, equal ones by index
         const int t = threadIdx.x;
         const int mine = t < a.B ? __ldcg(a.lengths + t) : 0;
-        int* all = reinterpret_cast<int*>(T.ml);
+        int* all = reinterpret_cast<int*>(sPart);
         if (t < a.B) all[t] = mine;
         __syncthreads();
         if (t < a.B) {
             int place = 0;
             for (int j = 0; j < a.B; ++j) place += all[j] > mine || (all[j] == mine && j < t);
-            if (place == b) T.par[0] = t;
+            T.lengths[place] = mine;
+            T.order[place] = static_cast<short>(t);
         }
-        __syncthreads();
-        b = T.par[0];
-        __syncthreads();
     }
-    const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && threadIdx.x == 0 ? a.status : nullptr);
-    const int n_cache = (len + KEYS - 1) / KEYS;   // tiles of the cache; tile n_cache is the nodes'
-    const int n_steps = rank <= n_cache ? (n_cache - rank) / a.cluster + 1 : 0;
-    const bool has_nodes = n_cache % a.cluster == rank;   // as the last step
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = T.tmem;
 
     if (warp == 0) {
         // ------------------------------------------------------------ loads
-        if (lane == 0 && n_steps > 0) {
-            mbar_arrive_expect_tx(&T.q_full, TILE);
-            for (int i = 0; i < KEYS / BOX; ++i)
-                tma_load_4d(sQ + i * (BOX * HS * 2), &tmNode, &T.q_full, 0, h, (i * BOX) % R, b);
-            int issued_k = 0, issued_v = 0;
-            for (int j = 0; j < n_steps; ++j) {
-                const int st = j % STAGES;
-                const uint32_t ph = (j / STAGES) & 1;
-                const int t = rank + j * a.cluster;
-                for (int v = 0; v < 2; ++v) {
-                    uint64_t* full = v ? &T.v_full[st] : &T.k_full[st];
-                    uint8_t* dst = (v ? sV : sK) + st * TILE;
-                    if (!mbar_wait(v ? &T.v_empty[st] : &T.k_empty[st], ph ^ 1u, abort_flag)) {
-                        j = n_steps;
+        if (lane == 0) {
+            int n = 0, n_q = 0;   // tiles and query loads issued
+            bool ok = true;
+            int issued_v = 0;
+            for (int round = 0; ok && pair_at(round) < n_pairs; ++round) {
+                const Work w = work_of<R>(pair_at(round), a, T, rank, nullptr);
+                for (int j = 0; ok && j < w.n_steps; ++j, ++n) {
+                    const int st = n % STAGES;
+                    const uint32_t ph = (n / STAGES) & 1;
+                    const int t = rank + j * a.cluster;
+                    auto tile = [&](int v) {
+                        uint64_t* full = v ? &T.v_full[st] : &T.k_full[st];
+                        uint8_t* dst = (v ? sV : sK) + st * TILE;
+                        if (!w.last(j)) {
+                            mbar_arrive_expect_tx(full, TILE);
+                            tma_load_4d(dst, &tmCache, full, 0, v * a.nh + w.h, t * KEYS, w.b);
+                            return;
+                        }
+                        const int boxes = (w.rest + BOX - 1) / BOX;
+                        mbar_arrive_expect_tx(full, (boxes + R / BOX) * BOX_BYTES);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_4d(dst + i * BOX_BYTES, &tmRest, full, 0, v * a.nh + w.h, t * KEYS + i * BOX, w.b);
+                        for (int i = 0; i < R / BOX; ++i)
+                            tma_load_4d(dst + ((KEYS - R) / BOX + i) * BOX_BYTES, &tmNode, full, 0, (1 + v) * a.nh + w.h, i * BOX, w.b);
+                    };
+                    if (!(ok = mbar_wait(&T.k_empty[st], ph ^ 1u, abort_flag))) break;
+                    tile(0);
+                    if (j == 0) {
+                        if (n_q > 0 && !mbar_wait(&T.q_empty, (n_q - 1) & 1, abort_flag)) {
+                            ok = false;
+                            ++n;
+                            break;
+                        }
+                        mbar_arrive_expect_tx(&T.q_full, TILE);
+                        for (int i = 0; i < KEYS / BOX; ++i)
+                            tma_load_4d(sQ + i * BOX_BYTES, &tmNode, &T.q_full, 0, w.h, (i * BOX) % R, w.b);
+                        ++n_q;
+                    }
+                    if (!mbar_wait(&T.v_empty[st], ph ^ 1u, abort_flag)) {
+                        ok = false;
+                        ++n;
                         break;
                     }
-                    if (t < n_cache) {
-                        mbar_arrive_expect_tx(full, TILE);
-                        tma_load_4d(dst, &tmCache, full, 0, v * a.nh + h, t * KEYS, b);
-                    } else {
-                        mbar_arrive_expect_tx(full, R * HS * 2);
-                        for (int i = 0; i < R / BOX; ++i)
-                            tma_load_4d(dst + i * (BOX * HS * 2), &tmNode, full, 0, (1 + v) * a.nh + h, i * BOX, b);
-                    }
-                    ++(v ? issued_v : issued_k);
+                    tile(1);
+                    ++issued_v;
                 }
             }
-            // No bulk copy may still target shared memory when the CTA exits.
-            mbar_drain(&T.q_full, 0);
+            // No bulk copy may still target shared memory when the CTA exits (n: K tiles issued).
+            if (n_q > 0) mbar_drain(&T.q_full, (n_q - 1) & 1);
             for (int i = 1; i <= STAGES; ++i) {
-                if (issued_k >= i) mbar_drain(&T.k_full[(issued_k - i) % STAGES], ((issued_k - i) / STAGES) & 1);
+                if (n >= i) mbar_drain(&T.k_full[(n - i) % STAGES], ((n - i) / STAGES) & 1);
                 if (issued_v >= i) mbar_drain(&T.v_full[(issued_v - i) % STAGES], ((issued_v - i) / STAGES) & 1);
             }
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        if (lane == 0 && n_steps > 0) {
-            constexpr uint32_t idesc_s = make_idesc_bf16(128, KEYS, false), idesc_sn = make_idesc_bf16(128, R, false);
-            constexpr uint32_t idesc_o = make_idesc_bf16(128, HS, true);
+        if (lane == 0) {
+            constexpr uint32_t idesc_s = make_idesc_bf16(128, KEYS, false), idesc_o = make_idesc_bf16(128, HS, true);
             const uint32_t tS = tmem + COL_S, tP = tmem + COL_P, tO = tmem + COL_O;
+            const uint32_t q_addr = smem_addr(sQ);
             // Testing aid (gpt_set_wait_limit_ns): nothing arrives on `drain` before the commit below.
             if (g_force_timeout) mbar_wait(&T.drain, 0, abort_flag);
-            const bool ok = !g_force_timeout && mbar_wait(&T.q_full, 0, abort_flag);
-            tc_fence_after();
-            const uint32_t q_addr = smem_addr(sQ);
-            for (int j = 0; ok && j <= n_steps; ++j) {
-                if (j < n_steps) {   // S_j, once the softmax has taken S_{j-1} out of TMEM
-                    const int st = j % STAGES;
-                    if (!mbar_wait(&T.k_full[st], (j / STAGES) & 1, abort_flag)) break;
-                    if (j > 0 && !mbar_wait(&T.s_free, (j - 1) & 1, abort_flag)) break;
+            bool ok = !g_force_timeout;
+            int n = 0, n_q = 0;
+            bool first = true;   // step n - 1 was its pair's first
+            auto values = [&]() {   // O (+)= P_{n-1} V_{n-1}, once the softmax has written P_{n-1}
+                const int st = (n - 1) % STAGES;
+                if (!mbar_wait(&T.p_full, (n - 1) & 1, abort_flag) ||
+                    !mbar_wait(&T.v_full[st], ((n - 1) / STAGES) & 1, abort_flag))
+                    return false;
+                tc_fence_after();
+                const uint32_t v_addr = smem_addr(sV + st * TILE);
+#pragma unroll
+                for (int kk = 0; kk < KEYS / 16; ++kk)
+                    umma_ts(tO, tP + kk * 8, make_sdesc_sw128(v_addr + kk * 2048), idesc_o, !first || kk > 0);
+                umma_commit(&T.v_empty[st]);
+                umma_commit(&T.o_done);
+                return true;
+            };
+            for (int round = 0; ok && pair_at(round) < n_pairs; ++round) {
+                const Work w = work_of<R>(pair_at(round), a, T, rank, nullptr);
+                for (int j = 0; j < w.n_steps; ++j, ++n) {
+                    // between pairs the values first: the softmax waits for them, not for the next scores
+                    if (j == 0 && n > 0 && !(ok = values())) break;
+                    if (j == 0 && !(ok = mbar_wait(&T.q_full, n_q++ & 1, abort_flag))) break;
+                    const int st = n % STAGES;
+                    // S_n, once the softmax has taken S_{n-1} out of TMEM
+                    if (!(ok = mbar_wait(&T.k_full[st], (n / STAGES) & 1, abort_flag))) break;
+                    if (n > 0 && !(ok = mbar_wait(&T.s_free, (n - 1) & 1, abort_flag))) break;
                     tc_fence_after();
                     const uint32_t k_addr = smem_addr(sK + st * TILE);
-                    const uint32_t idesc = has_nodes && j == n_steps - 1 ? idesc_sn : idesc_s;
 #pragma unroll
                     for (int kk = 0; kk < HS / 16; ++kk)
-                        umma_ss(tS, make_sdesc_sw128(q_addr + kk * 32), make_sdesc_sw128(k_addr + kk * 32), idesc, kk > 0);
+                        umma_ss(tS, make_sdesc_sw128(q_addr + kk * 32), make_sdesc_sw128(k_addr + kk * 32), idesc_s, kk > 0);
                     umma_commit(&T.k_empty[st]);
+                    if (j == w.n_steps - 1) umma_commit(&T.q_empty);
                     umma_commit(&T.s_full);
-                }
-                if (j > 0) {         // O += P_{j-1} V_{j-1}, once the softmax has written P_{j-1}
-                    const int jj = j - 1, st = jj % STAGES;
-                    if (!mbar_wait(&T.p_full, jj & 1, abort_flag)) break;
-                    if (!mbar_wait(&T.v_full[st], (jj / STAGES) & 1, abort_flag)) break;
-                    tc_fence_after();
-                    const uint32_t v_addr = smem_addr(sV + st * TILE);
-                    const int n_k = has_nodes && jj == n_steps - 1 ? R / 16 : KEYS / 16;
-                    for (int kk = 0; kk < n_k; ++kk)
-                        umma_ts(tO, tP + kk * 8, make_sdesc_sw128(v_addr + kk * 2048), idesc_o, jj > 0 || kk > 0);
-                    umma_commit(&T.v_empty[st]);
-                    umma_commit(&T.o_done);
+                    if (j > 0 && !(ok = values())) break;
+                    first = j == 0;
                 }
             }
+            if (ok && n > 0) values();
             umma_commit(&T.drain);
             mbar_drain(&T.drain, 0);
         }
-    }
-    // every node's A(i), while the first tiles travel (the issuing lanes pass through when they are done)
-    if (warp >= 2) {
+    } else {
+        // ------------------------------------------------------------ softmax and join
         const int t = threadIdx.x - 64;
-        if (t < a.N) T.par[t] = __ldcg(a.parents + static_cast<long long>(b) * a.N + t);
-        named_barrier(1, 128);
-        if (t < kMaxNodes) {
-            T.see[t] = t < a.N ? ancestors(T.par, t) : 0;
-            if (h == 0 && rank == 0 && t < a.N && T.see[t] == 0 && T.par[t] != -2) set_status(a.status, GPT_ERR_INDEX);
-        }
-        named_barrier(1, 128);
-
-        // ------------------------------------------------------------ softmax
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane, group = r / R, node = r % R, col0 = group * R;
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + COL_S + lane_off + col0, tP = tmem + COL_P + lane_off, tO = tmem + COL_O + lane_off;
-        const unsigned long long see = T.see[node];
-        float m_used = -INFINITY, l = 0.f;
-        bool ok = n_steps > 0;
-        if (ok) {
+        const bool node_group = group == KEYS / R - 1;
+        const long long C = static_cast<long long>(a.nh) * HS;
+        {
             uint32_t zero[32];
 #pragma unroll
             for (int i = 0; i < 32; ++i) zero[i] = 0;
             tmem_st32(tP, zero);
             tmem_st32(tP + 32, zero);
         }
-        for (int j = 0; ok && j < n_steps; ++j) {
-            const bool nodes = has_nodes && j == n_steps - 1;
-            const int st = j % STAGES;
-            const int keys = nodes ? R : len - (rank + j * a.cluster) * KEYS;   // of this tile
-            if (nodes || keys < KEYS) {
-                // V rows that must not matter
-                const bool got = mbar_wait(&T.v_full[st], (j / STAGES) & 1, abort_flag);
-                uint4* row = reinterpret_cast<uint4*>(sV + st * TILE + r * (HS * 2));
-                if (got && (nodes ? r < R && T.see[r & (kMaxNodes - 1)] == 0 : r >= keys)) {
+        int32_t* status = rank == 0 && t == 0 ? a.status : nullptr;
+        int n = 0;
+        bool ok = true, more = pair_at(0) < n_pairs;
+        Work next = {};
+        int next_parent = 0;
+        auto look_ahead = [&](int round) {   // the pair of that round, its parents on their way
+            more = pair_at(round) < n_pairs;
+            if (!more) return;
+            next = work_of<R>(pair_at(round), a, T, rank, status);
+            if (t < a.N) next_parent = __ldcg(a.parents + static_cast<long long>(next.b) * a.N + t);
+        };
+        look_ahead(0);
+        for (int round = 0; ok && more; ++round) {
+            const Work w = next;
+            if (t < a.N) T.par[t] = next_parent;
+            if (t == 0) T.bad = 0;
+            named_barrier(1, 128);
+            if (t < kMaxNodes) {
+                T.see[t] = t < a.N ? ancestors(T.par, t) : 0;
+                if (w.h == 0 && rank == 0 && t < a.N && T.see[t] == 0 && T.par[t] != -2) set_status(a.status, GPT_ERR_INDEX);
+            }
+            named_barrier(1, 128);
+            const unsigned long long see = T.see[node];
+            float m_used = -INFINITY, l = 0.f;
+            for (int j = 0; j < w.n_steps; ++j, ++n) {
+                const bool last = w.last(j);
+                const int st = n % STAGES;
+                const int keys = last ? w.rest : min(KEYS, w.len - (rank + j * a.cluster) * KEYS);   // of the cache
+                if (keys < KEYS) {
+                    // V rows that must not matter
+                    const bool got = mbar_wait(&T.v_full[st], (n / STAGES) & 1, abort_flag);
+                    uint4* row = reinterpret_cast<uint4*>(sV + st * TILE + r * (HS * 2));
+                    const bool is_node = last && node_group;
+                    if (got && (is_node ? see == 0 : r >= keys)) {
 #pragma unroll
-                    for (int i = 0; i < HS / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
-                } else if (got && nodes && r < R) {
-                    bool any = false;
+                        for (int i = 0; i < HS / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
+                    } else if (got && is_node) {
+                        bool any = false;
 #pragma unroll
-                    for (int i = 0; i < HS / 8; ++i) {
-                        uint32_t w[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
-                        bool here = false;
+                        for (int i = 0; i < HS / 8; ++i) {
+                            uint32_t v[4] = {row[i].x, row[i].y, row[i].z, row[i].w};
+                            bool here = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u, here = true;
-                            if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu, here = true;
+                            for (int e = 0; e < 4; ++e) {
+                                if ((v[e] & 0x7f80u) == 0x7f80u) v[e] &= 0xffff0000u, here = true;
+                                if ((v[e] & 0x7f800000u) == 0x7f800000u) v[e] &= 0xffffu, here = true;
+                            }
+                            if (here) row[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                            any |= here;
                         }
-                        if (here) row[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                        any |= here;
+                        if (any) atomicOr(&T.bad, 1ull << node);
                     }
-                    if (any) atomicOr(&T.bad, 1ull << r);
+                    fence_proxy_async_shared();
                 }
-                fence_proxy_async_shared();
-            }
-            const bool got = mbar_wait(&T.s_full, j & 1, abort_flag);
-            __syncwarp();   // tcgen05.ld / st are warp-collective
-            if (!__all_sync(0xffffffffu, got)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
-            float s[R];
-            {
-                uint32_t u[R];
-                if constexpr (R == 32) tmem_ld32(tS, u);
-                else tmem_ld64(tS, u);
+                const bool got = mbar_wait(&T.s_full, n & 1, abort_flag);
+                __syncwarp();   // tcgen05.ld / st are warp-collective
+                if (!__all_sync(0xffffffffu, got)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                float s[R];
+                {
+                    uint32_t u[R];
+                    if constexpr (R == 32) tmem_ld32(tS, u);
+                    else tmem_ld64(tS, u);
 #pragma unroll
-                for (int c = 0; c < R; ++c) s[c] = __uint_as_float(u[c]);
-            }
-            tc_fence_before();
-            mbar_arrive(&T.s_free);
-            const bool idle = nodes && group > 0;   // (warp-uniform)
-            uint32_t pk[R / 2];
-            float alpha = 1.f;
-            if (!idle) {
-                if (nodes) {
+                    for (int c = 0; c < R; ++c) s[c] = __uint_as_float(u[c]);
+                }
+                tc_fence_before();
+                mbar_arrive(&T.s_free);
+                if (last && node_group) {
 #pragma unroll
                     for (int c = 0; c < R; ++c)
                         if (!((see >> c) & 1)) s[c] = -INFINITY;
@@ -364,6 +466,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 #pragma unroll
                 for (int c = 4; c < R; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
                 const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                float alpha = 1.f;
                 if (mx > m_used + kRescaleThreshold || (m_used == -INFINITY && mx > -INFINITY)) {
                     alpha = m_used == -INFINITY ? 0.f : exp2_approx(m_used - mx);
                     m_used = mx;
@@ -371,6 +474,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const float off = m_used == -INFINITY ? 0.f : -m_used;   // nothing visible yet: 2^-inf
                 const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), off2 = f2_pack(off, off);
                 uint64_t acc[2] = {0, 0};
+                uint32_t pk[R / 2];
 #pragma unroll
                 for (int c = 0; c < R; c += 2) {
                     float x0, x1;
@@ -382,18 +486,17 @@ __global__ void __launch_bounds__(THREADS, 2)
                 float a0, a1;
                 f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
                 l = l * alpha + (a0 + a1);
-            }
-            // P_j may overwrite P_{j-1} and O may be rescaled only after O += P_{j-1} V_{j-1}.
-            if (j > 0) {
-                const bool done = mbar_wait(&T.o_done, (j - 1) & 1, abort_flag);
-                __syncwarp();
-                if (!__all_sync(0xffffffffu, done)) {
-                    ok = false;
-                    break;
+                // P_n may overwrite P_{n-1} and O may be rescaled only after O += P_{n-1} V_{n-1} (for a
+                // pair's first step the join before it has waited for that).
+                if (j > 0) {
+                    const bool done = mbar_wait(&T.o_done, (n - 1) & 1, abort_flag);
+                    __syncwarp();
+                    if (!__all_sync(0xffffffffu, done)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
                 }
-                tc_fence_after();
-            }
-            if (!idle) {
                 if constexpr (R == 32) tmem_st16(tP + group * (R / 2), pk);
                 else tmem_st32(tP + group * (R / 2), pk);
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -406,26 +509,72 @@ __global__ void __launch_bounds__(THREADS, 2)
                         tmem_st32(tO + c, u);
                     }
                 }
+                tc_fence_before();
+                mbar_arrive(&T.p_full);
             }
-            tc_fence_before();
-            mbar_arrive(&T.p_full);
-        }
-        const bool last = ok && mbar_wait(&T.o_done, (n_steps - 1) & 1, abort_flag);
-        __syncwarp();
-        float* out = reinterpret_cast<float*>(sK) + r * LD;   // every tile has been consumed
-        const bool done = __all_sync(0xffffffffu, last);
-        if (done) {
-            tc_fence_after();
+            look_ahead(round + 1);
+            bool have = false;
+            if (ok && w.n_steps > 0) {
+                const bool done = mbar_wait(&T.o_done, (n - 1) & 1, abort_flag);
+                __syncwarp();
+                ok = have = __all_sync(0xffffffffu, done);
+                tc_fence_after();
+            }
+            T.ml[r] = make_float2(m_used, have ? l : 0.f);
+
+            // The groups' parts joined: half rows at a time beside the ring while it fills for the next pair,
+            // whole rows in the ring's place after the last; alone, the CTA writes the rows.
+            bf16* out = y + static_cast<long long>(w.b) * a.N * C + w.h * HS;
+            const bf16* values = qkv + static_cast<long long>(w.b) * a.N * 3 * C + 2 * C + w.h * HS;
+            auto join = [&](const float* part, int ld, int d0, int pieces_log2) {
+                named_barrier(1, 128);
+                const unsigned long long bad = T.bad;
+                for (int it = t; it < a.N << pieces_log2; it += 128) {
+                    const int i = it >> pieces_log2, dp = (it & ((1 << pieces_log2) - 1)) * 8, d = d0 + dp;
+                    float2 ml[KEYS / R];
+                    Joined x;
 #pragma unroll
-            for (int c = 0; c < HS; c += 32) {
+                    for (int g = 0; g < KEYS / R; ++g) ml[g] = T.ml[g * R + i], x.see(ml[g]);
+#pragma unroll
+                    for (int g = 0; g < KEYS / R; ++g)
+                        if (ml[g].y != 0.f) {
+                            const float4* o = reinterpret_cast<const float4*>(part + (g * R + i) * ld + dp);
+                            x.add(ml[g], o[0], o[1]);
+                        }
+                    if (a.cluster > 1) {
+                        st8(joined + i * LD + d, x.o);
+                        if (d == 0) T.joined_ml[i] = make_float2(x.M, x.L);
+                    } else {
+                        if (T.see[i]) {
+                            x.finish(bad & T.see[i], values + d, 3 * C);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x.o[e] = 0.f;
+                        }
+                        st8(out + i * C + d, x.o);
+                    }
+                }
+            };
+            auto leave = [&](float* row, int d0) {   // 32 dimensions of this thread's row
                 uint32_t u[32];
-                tmem_ld32(tO + c, u);
+                tmem_ld32(tO + d0, u);
 #pragma unroll
-                for (int e = 0; e < 32; e += 4)
-                    *reinterpret_cast<uint4*>(out + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+                for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(row + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+            };
+            if (more) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    if (have) leave(sPart + r * HALF_LD, half * HALF);
+                    join(sPart, HALF_LD, half * HALF, 2);
+                    // (a time-out seen by one warp ends the rounds of all)
+                    ok = !named_barrier_or(1, 128, !ok);
+                }
+            } else {
+                float* whole = reinterpret_cast<float*>(sK);
+                if (have) leave(whole + r * LD, 0), leave(whole + r * LD + HALF, HALF);
+                join(whole, LD, 0, 3);
             }
         }
-        T.ml[r] = make_float2(m_used, done ? l : 0.f);
         tc_fence_before();
     }
 
@@ -435,57 +584,21 @@ __global__ void __launch_bounds__(THREADS, 2)
         tc_fence_after();
         tmem_dealloc(tmem, TMEM_COLS);
     }
-    // The groups joined within the CTA, then the CTAs.
-    const float* parts = reinterpret_cast<const float*>(sK);
-    float* joined = reinterpret_cast<float*>(sK) + KEYS * LD;
-    const long long C = static_cast<long long>(a.nh) * HS;
-    bf16* out = y + static_cast<long long>(b) * a.N * C + h * HS;
-    const bool alone = a.cluster == 1;
-    unsigned long long bad = T.bad;
-    auto finish = [&](int i, int d, Joined& j) {
-        j.finish();
-        for (unsigned long long todo = bad & T.see[i]; todo; todo &= todo - 1) {
-            const bf16* w = qkv + (static_cast<long long>(b) * a.N + __ffsll(todo) - 1) * 3 * C + 2 * C + h * HS + d;
-            float f[8];
-            ld8(w, f);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (!isfinite(f[e])) j.o[e] += f[e];
-        }
-    };
-    for (int it = threadIdx.x; it < a.N * (HS / 8); it += THREADS) {
-        const int i = it / (HS / 8), d = it % (HS / 8) * 8;
-        float2 ml[KEYS / R];
-        Joined j;
-#pragma unroll
-        for (int g = 0; g < KEYS / R; ++g) ml[g] = T.ml[g * R + i], j.see(ml[g]);
-#pragma unroll
-        for (int g = 0; g < KEYS / R; ++g)
-            if (ml[g].y != 0.f) {
-                const float4* o = reinterpret_cast<const float4*>(parts + (g * R + i) * LD + d);
-                j.add(ml[g], o[0], o[1]);
-            }
-        if (alone) {
-            if (T.see[i]) {
-                finish(i, d, j);
-            } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) j.o[e] = 0.f;
-            }
-            st8(out + i * C + d, j.o);
-        } else {
-            st8(joined + i * LD + d, j.o);
-            if (d == 0) T.joined_ml[i] = make_float2(j.M, j.L);
-        }
-    }
     if (threadIdx.x == 0 && *abort_flag) set_status(a.status, GPT_ERR_TIMEOUT);
-    if (alone) return;
+    if (a.cluster == 1) return;
+    // A cluster has one pair: its CTAs' parts joined.
     __syncwarp();
     cluster_sync();
-    const int holder = n_cache % a.cluster;   // of the nodes' tile
-    bad = static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&T.bad) + 1, holder))) << 32 |
-          ld_cluster_u32(map_to_rank(&T.bad, holder));
-    join_cluster(joined, LD, T.joined_ml, T.see, a, HS / 8, rank, out, C, finish);
+    const Work w = work_of<R>(pair0, a, T, rank, nullptr);
+    const int holder = w.n_cache % a.cluster;   // of the nodes' tile
+    const unsigned long long bad =
+        static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&T.bad) + 1, holder))) << 32 |
+        ld_cluster_u32(map_to_rank(&T.bad, holder));
+    const long long C = static_cast<long long>(a.nh) * HS;
+    const bf16* values = qkv + static_cast<long long>(w.b) * a.N * 3 * C + 2 * C + w.h * HS;
+    join_cluster(joined, LD, T.joined_ml, T.see, a, HS / 8, rank,
+                 y + static_cast<long long>(w.b) * a.N * C + w.h * HS, C,
+                 [&](int i, int d, Joined& x) { x.finish(bad & T.see[i], values + d, 3 * C); });
     __syncwarp();
     cluster_sync();   // no CTA leaves while another reads its part
 }
@@ -730,10 +843,10 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
     a.cluster = 1;
     const long long slots = 148 * (f32 ? 5 : 2);   // CTAs that run at a time
     while (a.cluster < 8 && pairs * a.cluster * 2 <= slots && a.cluster < tiles) a.cluster *= 2;
-    if (getenv("TREE_CL")) a.cluster = atoi(getenv("TREE_CL"));
     // more CTAs than run at a time: those with the most work start first
     a.longest_first = !f32 && B > 1 && B <= tc::THREADS && pairs * a.cluster > slots;
-    const dim3 grid(static_cast<unsigned>(pairs * a.cluster));
+    // bf16 without clusters: persistent CTAs
+    const dim3 grid(static_cast<unsigned>((f32 || a.cluster > 1 || pairs < slots ? pairs : slots) * a.cluster));
     if (f32) return hs <= 64 ? simt::launch<1>(qkv, kv, y, a, grid.x, s) : simt::launch<2>(qkv, kv, y, a, grid.x, s);
     int rc;
     // {hs, heads of q, k, v (nodes) or k, v (cache), rows, sequences}
@@ -744,16 +857,18 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
     const uint64_t cache_dims[4] = {64, static_cast<uint64_t>(2) * nh, static_cast<uint64_t>(block_size), static_cast<uint64_t>(B)};
     const uint64_t cache_strides[3] = {128, 2 * C2, 2 * C2 * block_size};
     const uint32_t cache_box[4] = {64, 1, tc::KEYS, 1};
-    CUtensorMap node_map, cache_map;
+    const uint32_t rest_box[4] = {64, 1, tc::BOX, 1};
+    CUtensorMap node_map, cache_map, rest_map;
     rc = make_tmap_bf16_4d(&node_map, qkv, node_dims, node_strides, node_box);
     if (!rc) rc = make_tmap_bf16_4d(&cache_map, kv, cache_dims, cache_strides, cache_box);
+    if (!rc) rc = make_tmap_bf16_4d(&rest_map, kv, cache_dims, cache_strides, rest_box);
     if (rc) return rc;
     static size_t opted32[kMaxDevices] = {}, opted64[kMaxDevices] = {};
     auto kern = N <= 32 ? tc::tree_attention_tc<32> : tc::tree_attention_tc<64>;
     rc = N <= 32 ? opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted32)
                  : opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted64);
     if (rc) return rc;
-    return launch_overlapped_cluster(kern, a.cluster, grid, dim3(tc::THREADS), tc::SMEM, s, node_map, cache_map,
+    return launch_overlapped_cluster(kern, a.cluster, grid, dim3(tc::THREADS), tc::SMEM, s, node_map, cache_map, rest_map,
                                      static_cast<const bf16*>(qkv), static_cast<bf16*>(y), a);
 }
 
