@@ -45,11 +45,12 @@ __global__ void tree_embed_kernel(const E* __restrict__ wte, const E* __restrict
 // A cluster of kAcceptCtas CTAs per sequence.  The first warp of every CTA finds the path (a lane per
 // pair of nodes: with M the set of nodes that match their parent's choice, node i is accepted iff
 // A(i) is inside M; the path is A of the accepted node with the most ancestors, and its nodes in
-// index order run from the root down); then the cluster's threads copy the path's k and v rows of
-// every layer, 16 bytes each.  All CTAs have read the length before the cluster barrier, so
+// index order run from the root down); then the cluster's warps copy the path's k and v rows of
+// every layer, a row at a time with 8 loads of 16 bytes per lane in flight.  All CTAs have read the length before the cluster barrier, so
 // lengths_out may be lengths itself.
 constexpr int kAcceptCtas = 8;
 constexpr int kAcceptThreads = 256;
+constexpr int kAcceptLoads = 8;
 
 __global__ void __launch_bounds__(kAcceptThreads)
     tree_accept_kernel(const int* __restrict__ parents, const int64_t* __restrict__ tok,
@@ -108,15 +109,24 @@ __global__ void __launch_bounds__(kAcceptThreads)
     __syncthreads();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const int n = s_n, len = s_len;
-    const int per_row = static_cast<int>(2 * c_bytes / 16);
-    const int total = n_layer * n * per_row;
-    for (int u = rank * kAcceptThreads + tid; u < total; u += kAcceptCtas * kAcceptThreads) {
-        const int row = u / per_row, off = (u % per_row) * 16;
-        const int l = row / n, j = row % n;
-        const uint8_t* src = tree_qkv + ((static_cast<long long>(l) * B + b) * N + way[j]) * 3 * c_bytes + c_bytes + off;
-        uint8_t* dst = cache + ((static_cast<long long>(l) * B + b) * block_size + len + j) * 2 * c_bytes + off;
-        *reinterpret_cast<uint4*>(dst) = __ldcg(reinterpret_cast<const uint4*>(src));
+    const int units = static_cast<int>(2 * c_bytes / 16);   // of a row's k and v
+    const int warps = kAcceptCtas * kAcceptThreads / 32, lane = tid & 31;
+    for (int row = rank * (kAcceptThreads / 32) + (tid >> 5); row < n_layer * n; row += warps) {
+        const int l = row / n, j = row - l * n;
+        const uint4* src = reinterpret_cast<const uint4*>(
+            tree_qkv + ((static_cast<long long>(l) * B + b) * N + way[j]) * 3 * c_bytes + c_bytes);
+        uint4* dst = reinterpret_cast<uint4*>(cache + ((static_cast<long long>(l) * B + b) * block_size + len + j) * 2 * c_bytes);
+        for (int u0 = lane; u0 < units; u0 += 32 * kAcceptLoads) {
+            uint4 w[kAcceptLoads];
+#pragma unroll
+            for (int x = 0; x < kAcceptLoads; ++x)
+                if (u0 + 32 * x < units) w[x] = __ldcg(src + u0 + 32 * x);
+#pragma unroll
+            for (int x = 0; x < kAcceptLoads; ++x)
+                if (u0 + 32 * x < units) dst[u0 + 32 * x] = w[x];
+        }
     }
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank == 0 && tid == 0) lengths_out[b] = len + n;
 }

@@ -8,6 +8,7 @@ if the library cannot be loaded, importing this module raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 from typing import NamedTuple
@@ -544,17 +545,17 @@ def _launch(where: str, index: int, *args) -> None:
         raise GPTError(rc, where)
 
 
-def _cfg_ref(cfg: GPTConfig):
-    """byref of cfg's C form, made once per (frozen) configuration."""
-    kept = cfg.__dict__.get("_cref")
-    if kept is None:
-        kept = ctypes.byref(cfg.c())
-        cfg.__dict__["_cref"] = kept
-    return kept
+class _Kept(NamedTuple):
+    ref: object            # byref of the C form
+    dtype: torch.dtype
+    kv_bytes: int          # of one sequence's cache
 
 
-def _kv_bytes(cfg: GPTConfig, B: int) -> int:
-    return cfg.n_layer * B * cfg.block_size * 2 * cfg.n_embd * cfg.torch_dtype.itemsize
+@functools.lru_cache(maxsize=64)
+def _kept(cfg: GPTConfig) -> _Kept:
+    """What the calls below need of a (frozen) configuration, made once."""
+    dt = cfg.torch_dtype
+    return _Kept(ctypes.byref(cfg.c()), dt, cfg.n_layer * cfg.block_size * 2 * cfg.n_embd * dt.itemsize)
 
 
 def kv_layers(cfg: GPTConfig, kv_cache: torch.Tensor, B: int) -> torch.Tensor:
@@ -595,12 +596,13 @@ def tree_step(cfg: GPTConfig, weights: torch.Tensor, tok: torch.Tensor, parents:
     """gpt_tree_step: tok int64 [B, N], parents int32 [B, N], lengths int32 [B]; fills tree_qkv
     (alloc_tree_qkv) and returns the nodes' logits [B, N, V] in cfg's dtype."""
     B, N = tok.shape
-    index, dt, dev = _cuda_index(tok), cfg.torch_dtype, tok.device
+    kept = _kept(cfg)
+    index, dt, dev = _cuda_index(tok), kept.dtype, tok.device
     if logits is None:
         logits = torch.empty((B, N, cfg.vocab_size), dtype=dt, device=dev)
-    _launch("gpt_tree_step", index, _cfg_ref(cfg), _ptr(weights), _arg("tok", tok, torch.int64, (B, N), dev),
+    _launch("gpt_tree_step", index, kept.ref, _ptr(weights), _arg("tok", tok, torch.int64, (B, N), dev),
             _arg("parents", parents, torch.int32, (B, N), dev), _arg("lengths", lengths, torch.int32, (B,), dev), B, N,
-            _buffer("kv_cache", kv_cache, _kv_bytes(cfg, B), dev),
+            _buffer("kv_cache", kv_cache, B * kept.kv_bytes, dev),
             _arg("tree_qkv", tree_qkv, dt, (cfg.n_layer, B, N, 3, cfg.n_embd), dev),
             _arg("logits", logits, dt, (B, N, cfg.vocab_size), dev), _buffer("workspace", workspace, 0, dev),
             workspace.numel(), _stream_of(index, stream), GPT_FLAG_SYNC_CHECK if sync_check else 0)
@@ -620,17 +622,17 @@ def tree_accept(cfg: GPTConfig, parents: torch.Tensor, tok: torch.Tensor, chosen
     """gpt_tree_accept: keeps the drafted path that `chosen` confirms and copies its k, v into the cache.
     out: buffers to write (out.lengths may be `lengths` itself)."""
     B, N = parents.shape
-    index, dev, i32 = _cuda_index(parents), parents.device, torch.int32
+    kept = _kept(cfg)
+    index, dev, i32, i64 = _cuda_index(parents), parents.device, torch.int32, torch.int64
     if out is None:
-        n, new = parents.new_empty((2, B)).unbind(0)
-        out = TreeAccept(parents.new_empty((B, N)), n, torch.empty(B, dtype=torch.int64, device=dev), new)
-    _launch("gpt_tree_accept", index, _cfg_ref(cfg), _arg("parents", parents, i32, (B, N), dev),
-            _arg("tok", tok, torch.int64, (B, N), dev), _arg("chosen", chosen, torch.int64, (B, N), dev),
+        out = TreeAccept(torch.empty_like(parents), torch.empty_like(lengths), torch.empty(B, dtype=i64, device=dev),
+                         torch.empty_like(lengths))
+    _launch("gpt_tree_accept", index, kept.ref, _arg("parents", parents, i32, (B, N), dev),
+            _arg("tok", tok, i64, (B, N), dev), _arg("chosen", chosen, i64, (B, N), dev),
             _arg("lengths", lengths, i32, (B,), dev), B, N,
-            _arg("tree_qkv", tree_qkv, cfg.torch_dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), dev),
-            _buffer("kv_cache", kv_cache, _kv_bytes(cfg, B), dev), _arg("path", out.path, i32, (B, N), dev),
-            _arg("n_accepted", out.n_accepted, i32, (B,), dev),
-            _arg("next_token", out.next_token, torch.int64, (B,), dev),
+            _arg("tree_qkv", tree_qkv, kept.dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), dev),
+            _buffer("kv_cache", kv_cache, B * kept.kv_bytes, dev), _arg("path", out.path, i32, (B, N), dev),
+            _arg("n_accepted", out.n_accepted, i32, (B,), dev), _arg("next_token", out.next_token, i64, (B,), dev),
             _arg("lengths_out", out.lengths, i32, (B,), dev), _status_arg(status, dev), _stream_of(index, stream))
     return out
 
@@ -667,21 +669,22 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: 
     padded vocabulary), tokens int64 [rows] (-1: none).  out: buffers to write."""
     ptr, ld = _rows("logits", logits, logits)
     rows, V = logits.shape
-    index, dev, f32 = _cuda_index(logits), logits.device, torch.float32
+    index, dev, f32, i64 = _cuda_index(logits), logits.device, torch.float32, torch.int64
     if out is None:
-        logp, entropy, lse = torch.empty((3, rows), dtype=f32, device=dev).unbind(0)
+        logp, entropy, lse = torch.empty(3, rows, dtype=f32, device=dev).unbind(0)
         out = TokenLogprobs(logp if tokens is not None else None, entropy, lse,
-                            torch.empty((rows, k), dtype=torch.int64, device=dev) if k else None,
-                            torch.empty((rows, k), dtype=f32, device=dev) if k else None)
+                            torch.empty(rows, k, dtype=i64, device=dev) if k else None,
+                            torch.empty(rows, k, dtype=f32, device=dev) if k else None)
     if rows:
+        logp, entropy, lse, ids, top = out
         _launch("gpt_token_logprobs", index, ptr, ld,
-                None if tokens is None else _arg("tokens", tokens, torch.int64, (rows,), dev), rows, V,
+                None if tokens is None else _arg("tokens", tokens, i64, (rows,), dev), rows, V,
                 _STORED[logits.dtype], float(temperature),
-                None if out.logp is None else _arg("logp", out.logp, f32, (rows,), dev),
-                None if out.entropy is None else _arg("entropy", out.entropy, f32, (rows,), dev),
-                None if out.lse is None else _arg("lse", out.lse, f32, (rows,), dev), int(k),
-                None if out.top_ids is None else _arg("top_ids", out.top_ids, torch.int64, (rows, k), dev),
-                None if out.top_logp is None else _arg("top_logp", out.top_logp, f32, (rows, k), dev),
+                None if logp is None else _arg("logp", logp, f32, (rows,), dev),
+                None if entropy is None else _arg("entropy", entropy, f32, (rows,), dev),
+                None if lse is None else _arg("lse", lse, f32, (rows,), dev), int(k),
+                None if ids is None else _arg("top_ids", ids, i64, (rows, k), dev),
+                None if top is None else _arg("top_logp", top, f32, (rows, k), dev),
                 _status_arg(status, dev), _stream_of(index, stream))
     return out
 
