@@ -11,7 +11,8 @@ namespace gpt {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;          // 16-byte loads in flight per thread
+constexpr int kUnrollLog2 = 2;
+constexpr int kUnroll = 1 << kUnrollLog2;   // 16-byte loads in flight per thread
 constexpr int kMaxCluster = 8;
 constexpr int kCandidates = 512;    // places for the values at or above a part's top-k bound
 constexpr int kHits = 512;          // places for the steps that reach the bound
@@ -220,33 +221,48 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
     __shared__ uint32_t s_bound, s_hits;
     __shared__ int s_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ncta = a.cluster;
+    const int ncta = NT == 128 ? 1 : a.cluster;   // (known to the compiler for CTAs that are alone)
     const int rank = ncta > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     if (ncta > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const long long r = blockIdx.x / ncta;
     const Slice<E> row(logits + r * a.ld, a.V, ncta * NT);
     const uint32_t first = rank * NT + tid;
     griddep_wait();
+    // what is needed at the end travels with the row: the token's logit, the element outside the units
+    long long tok = -1;
+    if (a.logp && first == 0) tok = __ldcg(a.tokens + r);
+    const float z_end = first < row.ends ? ld_act(row.z + row.end_col(first)) : 0.f;
+    float z_tok = 0.f;
+    if (tok >= 0 && tok < a.V) z_tok = ld_act(row.z + tok);
     Running run = {a.floor_z, a.floor_z * a.c, 0, 0};
     if (a.k > 0 && a.slot_shift)
         for (int j = 0; j < kSlots; ++j) slots[j][tid] = static_cast<uint16_t>(a.floor2);
+    const uint32_t mine = first < row.units ? (row.units - first - 1) / row.stride + 1 : 0;   // this thread's units
     uint32_t step = 0;
-    for (uint32_t u0 = first; u0 < row.units; u0 += row.stride * kUnroll, ++step) {
-        uint4 w[kUnroll];
-#pragma unroll
-        for (int i = 0; i < kUnroll; ++i) {
-            const uint32_t u = u0 + i * row.stride;
-            const uint32_t f = sizeof(E) == 4 ? __float_as_uint(a.floor_z) : a.floor2;
-            w[i] = u < row.units ? __ldcg(reinterpret_cast<const uint4*>(row.z + row.unit_col(u))) : make_uint4(f, f, f, f);
-        }
+    auto finish_step = [&](const uint4(&w)[kUnroll]) {
         const float top = take(run, w, a.floor_z, a.floor2, a.c, row.z);
         if (a.k > 0) {
             uint16_t& slot = slots[step >> a.slot_shift][tid];
             if (a.slot_shift == 0 || key16(top) > key16(slot_value(slot))) slot = static_cast<uint16_t>(__float_as_uint(top) >> 16);
         }
+        ++step;
+    };
+    const uint4* units = reinterpret_cast<const uint4*>(row.z + row.head) + first;
+    for (uint32_t n = mine / kUnroll; n > 0; --n, units += kUnroll * row.stride) {
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) w[i] = __ldcg(units + i * row.stride);
+        finish_step(w);
+    }
+    if (mine % kUnroll) {
+        const uint32_t f = sizeof(E) == 4 ? __float_as_uint(a.floor_z) : a.floor2;
+        uint4 w[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i) w[i] = i < mine % kUnroll ? __ldcg(units + i * row.stride) : make_uint4(f, f, f, f);
+        finish_step(w);
     }
     if (first < row.ends) {
-        const float z = max_nan(ld_act(row.z + row.end_col(first)), a.floor_z);
+        const float z = max_nan(z_end, a.floor_z);
         run.raise(z, a.c);
         const float e = fmaf(z, a.c, -run.ref), p = exp2_approx(e);
         run.s = f2_add(run.s, f2_pack(p, 0.f));
@@ -330,27 +346,36 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
         const uint32_t bound16 = s_bound;
         const float bound = bound16 == 0 ? -INFINITY : bound16 == 0xffffu ? INFINITY : key_value(bound16 << 16);
         auto push = [&](float z, uint32_t col) {
-            if (!(z < bound)) {
-                const int at = atomicAdd(&s_count, 1);
-                if (at < kCandidates) cand[at] = entry(z, col);
-            }
+            const int at = atomicAdd(&s_count, 1);
+            if (at < kCandidates) cand[at] = entry(z, col);
         };
         if (my_key >= bound16) {   // this thread's steps that reach the bound
+            unsigned long long in = 0;   // (at most 64 slots)
             const uint32_t n = (step + (1u << a.slot_shift) - 1) >> a.slot_shift;
-            for (uint32_t j = 0; j < n; ++j)
-                if (key16(slot_value(slots[j][tid])) >= bound16) {
-                    const uint32_t at = atomicAdd(&s_hits, 1u);
-                    if (at < kHits) hits[at] = j << 16 | tid;
-                }
-            if (first < row.ends) push(ld_act(row.z + row.end_col(first)), row.end_col(first));
+#pragma unroll 4
+            for (uint32_t j = 0; j < n; ++j) in |= static_cast<unsigned long long>(!(slot_value(slots[j][tid]) < bound)) << j;
+            for (; in; in &= in - 1) {
+                const uint32_t at = atomicAdd(&s_hits, 1u);
+                if (at < kHits) hits[at] = static_cast<uint32_t>(__ffsll(in) - 1) << 16 | tid;
+            }
+            if (first < row.ends && !(z_end < bound)) push(z_end, row.end_col(first));
         }
         __syncthreads();
-        const uint32_t n_hits = s_hits, each = static_cast<uint32_t>(kUnroll) << a.slot_shift;
+        const uint32_t n_hits = s_hits, each_log2 = kUnrollLog2 + a.slot_shift;
         if (n_hits <= kHits)
-            for (uint32_t i = tid; i < n_hits * each; i += NT) {   // a unit each
-                const uint32_t hit = hits[i / each];
-                const uint32_t u = rank * NT + (hit & 0xffffu) + ((hit >> 16) * each + i % each) * row.stride;
-                if (u < row.units) row.unit(u, push);
+            for (uint32_t i = tid; i < n_hits << each_log2; i += NT) {   // a unit each
+                const uint32_t hit = hits[i >> each_log2];
+                const uint32_t u = rank * NT + (hit & 0xffffu) + (((hit >> 16) << each_log2) + (i & ((1u << each_log2) - 1))) * row.stride;
+                if (u >= row.units) continue;
+                const uint4 w = __ldcg(reinterpret_cast<const uint4*>(row.z + row.unit_col(u)));
+                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+                uint32_t in = 0, e = 0;
+                row.values(w, 0, [&](float z, uint32_t) { in |= static_cast<uint32_t>(!(z < bound)) << e++; });
+                for (; in; in &= in - 1) {
+                    const uint32_t at = __ffs(in) - 1, pos = sizeof(E) == 4 ? at : at >> 1;
+                    const uint32_t bits = pos == 0 ? x[0] : pos == 1 ? x[1] : pos == 2 ? x[2] : x[3];
+                    push(__uint_as_float(sizeof(E) == 4 ? bits : (at & 1) ? bits & 0xffff0000u : bits << 16), row.unit_col(u) + at);
+                }
             }
         __syncthreads();
         int count = s_count;
@@ -433,9 +458,8 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
         if (a.lse) a.lse[r] = none ? -INFINITY : static_cast<float>((ref + log2_s) * ln2);
         if (a.entropy) a.entropy[r] = none ? nan : static_cast<float>(ln2 * (log2_s - t / s));
         if (a.logp) {
-            const long long tok = __ldcg(a.tokens + r);
             float v = 0.f;
-            if (tok >= 0 && tok < a.V) v = logprob(ld_act(row.z + tok));
+            if (tok >= 0 && tok < a.V) v = logprob(z_tok);
             else if (tok != -1) set_status(a.status, GPT_ERR_INDEX);
             a.logp[r] = v;
         }
