@@ -54,6 +54,17 @@ GPT_DEVINL bool named_barrier_or(int id, int threads, bool v) {
     return r != 0;
 }
 
+// One lane of a converged warp.
+GPT_DEVINL bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // Parts of a softmax over disjoint keys: weighted values o (eight of a row), {maximum (log2 units), sum}.
 // A part without keys has a sum of 0 and its o is not looked at.
 struct Joined {
@@ -317,55 +328,62 @@ __global__ void __launch_bounds__(THREADS, 2)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------ products
-        if (lane == 0) {
-            constexpr uint32_t idesc_s = make_idesc_bf16(128, KEYS, false), idesc_o = make_idesc_bf16(128, HS, true);
-            const uint32_t tS = tmem + COL_S, tP = tmem + COL_P, tO = tmem + COL_O;
-            const uint32_t q_addr = smem_addr(sQ);
-            // Testing aid (gpt_set_wait_limit_ns): nothing arrives on `drain` before the commit below.
-            if (g_force_timeout) mbar_wait(&T.drain, 0, abort_flag);
-            bool ok = !g_force_timeout;
-            int n = 0, n_q = 0;
-            bool first = true;   // step n - 1 was its pair's first
-            auto values = [&]() {   // O (+)= P_{n-1} V_{n-1}, once the softmax has written P_{n-1}
-                const int st = (n - 1) % STAGES;
-                if (!mbar_wait(&T.p_full, (n - 1) & 1, abort_flag) ||
-                    !mbar_wait(&T.v_full[st], ((n - 1) / STAGES) & 1, abort_flag))
-                    return false;
-                tc_fence_after();
-                const uint32_t v_addr = smem_addr(sV + st * TILE);
+        // The whole warp follows the steps (uniform addresses and descriptors), one lane issues.
+        constexpr uint32_t idesc_s = make_idesc_bf16(128, KEYS, false), idesc_o = make_idesc_bf16(128, HS, true);
+        const uint32_t tS = tmem + COL_S, tP = tmem + COL_P, tO = tmem + COL_O;
+        const uint32_t q_addr = smem_addr(sQ), k_addr = smem_addr(sK), v_addr = smem_addr(sV);
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
+        };
+        // Testing aid (gpt_set_wait_limit_ns): nothing arrives on `drain` before the commit below.
+        if (g_force_timeout) wait(&T.drain, 0);
+        bool ok = !g_force_timeout;
+        int n = 0, n_q = 0;
+        bool first = true;   // step n - 1 was its pair's first
+        auto values = [&]() {   // O (+)= P_{n-1} V_{n-1}, once the softmax has written P_{n-1}
+            const int st = (n - 1) % STAGES;
+            if (!wait(&T.p_full, (n - 1) & 1) || !wait(&T.v_full[st], ((n - 1) / STAGES) & 1)) return false;
+            tc_fence_after();
+            if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < KEYS / 16; ++kk)
-                    umma_ts(tO, tP + kk * 8, make_sdesc_sw128(v_addr + kk * 2048), idesc_o, !first || kk > 0);
+                    umma_ts(tO, tP + kk * 8, make_sdesc_sw128(v_addr + st * TILE + kk * 2048), idesc_o, !first || kk > 0);
                 umma_commit(&T.v_empty[st]);
                 umma_commit(&T.o_done);
-                return true;
-            };
-            for (int round = 0; ok && pair_at(round) < n_pairs; ++round) {
-                const Work w = work_of<R>(pair_at(round), a, T, rank, nullptr);
-                for (int j = 0; j < w.n_steps; ++j, ++n) {
-                    // between pairs the values first: the softmax waits for them, not for the next scores
-                    if (j == 0 && n > 0 && !(ok = values())) break;
-                    if (j == 0 && !(ok = mbar_wait(&T.q_full, n_q++ & 1, abort_flag))) break;
-                    const int st = n % STAGES;
-                    // S_n, once the softmax has taken S_{n-1} out of TMEM
-                    if (!(ok = mbar_wait(&T.k_full[st], (n / STAGES) & 1, abort_flag))) break;
-                    if (n > 0 && !(ok = mbar_wait(&T.s_free, (n - 1) & 1, abort_flag))) break;
-                    tc_fence_after();
-                    const uint32_t k_addr = smem_addr(sK + st * TILE);
+            }
+            __syncwarp();
+            return true;
+        };
+        for (int round = 0; ok && pair_at(round) < n_pairs; ++round) {
+            const Work w = work_of<R>(pair_at(round), a, T, rank, nullptr);
+            for (int j = 0; j < w.n_steps; ++j, ++n) {
+                // between pairs the values first: the softmax waits for them, not for the next scores
+                if (j == 0 && n > 0 && !(ok = values())) break;
+                if (j == 0 && !(ok = wait(&T.q_full, n_q++ & 1))) break;
+                const int st = n % STAGES;
+                // S_n, once the softmax has taken S_{n-1} out of TMEM
+                if (!(ok = wait(&T.k_full[st], (n / STAGES) & 1))) break;
+                if (n > 0 && !(ok = wait(&T.s_free, (n - 1) & 1))) break;
+                tc_fence_after();
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < HS / 16; ++kk)
-                        umma_ss(tS, make_sdesc_sw128(q_addr + kk * 32), make_sdesc_sw128(k_addr + kk * 32), idesc_s, kk > 0);
+                        umma_ss(tS, make_sdesc_sw128(q_addr + kk * 32), make_sdesc_sw128(k_addr + st * TILE + kk * 32), idesc_s, kk > 0);
                     umma_commit(&T.k_empty[st]);
                     if (j == w.n_steps - 1) umma_commit(&T.q_empty);
                     umma_commit(&T.s_full);
-                    if (j > 0 && !(ok = values())) break;
-                    first = j == 0;
                 }
+                __syncwarp();
+                if (j > 0 && !(ok = values())) break;
+                first = j == 0;
             }
-            if (ok && n > 0) values();
+        }
+        if (ok && n > 0) values();
+        if (elect_one()) {
             umma_commit(&T.drain);
             mbar_drain(&T.drain, 0);
         }
+        __syncwarp();
     } else {
         // ------------------------------------------------------------ softmax and join
         const int t = threadIdx.x - 64;
