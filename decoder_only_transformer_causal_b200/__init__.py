@@ -85,6 +85,29 @@ class GPT:
         return native.generate(self.cfg, self.weights, idx, max_new_tokens, uniforms, temperature, top_k,
                                kv_cache=self._host[key], workspace=ws, step_logits=step_logits)
 
+    def score(self, idx: torch.Tensor, targets: torch.Tensor, k: int = 0, temperature: float = 1.0):
+        """Log probabilities of targets int64 [B, T] (-1: not scored) after idx [B, T], with each position's
+        entropy and, for k > 0, its k likeliest tokens: a native.TokenLogprobs of [B, T] (and [B, T, k])
+        tensors."""
+        B, T = idx.shape
+        logits, _ = self(idx, targets)
+        r = native.token_logprobs(logits.view(B * T, -1), targets.reshape(-1), k=k, temperature=temperature)
+        return native.TokenLogprobs(*(None if t is None else t.view(B, T, *t.shape[1:]) for t in r))
+
+    def verify(self, tok: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor, kv_cache: torch.Tensor):
+        """One greedy step over drafted trees: runs the nodes tok int64 [B, N] (parents int32 [B, N], -1 for a
+        root, -2 for no node) over the cache's first lengths int32 [B] positions, takes the likeliest token at
+        each node, and keeps the path that the choices confirm (its k, v go into the cache).  Returns
+        (native.TreeAccept, chosen int64 [B, N]); the kept tokens are chosen along the path."""
+        B, N = tok.shape
+        key = ("tree", B, N)
+        if key not in self._host:
+            self._host[key] = native.alloc_tree_qkv(self.cfg, B, N, self.device)
+        logits = native.tree_step(self.cfg, self.weights, tok, parents, lengths, kv_cache, self._host[key],
+                                  self.workspace(B, N))
+        chosen = native.token_logprobs(logits.view(B * N, -1), None, k=1).top_ids.view(B, N)
+        return native.tree_accept(self.cfg, parents, tok, chosen, lengths, self._host[key], kv_cache), chosen
+
 
 class AdamW:
     """Optimizer state for a GPT's packed parameters ("nanoGPT 全局流程图", 3.5 and 3.6,

@@ -106,6 +106,14 @@ int make_tmap_bf16_4d(CUtensorMap* m, const void* base, const uint64_t dims[4], 
     return encode(m, base, 4, d, s, b);
 }
 
+int make_tmap_f32_4d(CUtensorMap* m, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
+                     const uint32_t box[4]) {
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+    const cuuint64_t s[3] = {strides_bytes[0], strides_bytes[1], strides_bytes[2]};
+    const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+    return encode(m, base, 4, d, s, b, CU_TENSOR_MAP_DATA_TYPE_FLOAT32);
+}
+
 }  // namespace gpt
 
 using namespace gpt;

@@ -78,6 +78,8 @@ int make_tmap_2d_sw64(CUtensorMap* m, const void* base, bool fp32, uint64_t inne
                       uint64_t row_stride_bytes, uint32_t box_inner, uint32_t box_outer);
 int make_tmap_bf16_4d(CUtensorMap* m, const void* base, const uint64_t dims[4],
                       const uint64_t strides_bytes[3], const uint32_t box[4]);
+int make_tmap_f32_4d(CUtensorMap* m, const void* base, const uint64_t dims[4], const uint64_t strides_bytes[3],
+                     const uint32_t box[4]);
 
 // ---- row-wise kernels (rowwise.cu)
 int launch_embed(const void* wte, const void* wpe, const int64_t* idx, float* x, int B, int T,

@@ -8,7 +8,6 @@
 // softmax (running maximum, sum and weighted values, all fp32), and the parts are joined over distributed
 // shared memory in a fixed order, so the call needs no workspace and its results are reproducible.
 #include <math.h>
-#include <type_traits>
 
 #include "internal.h"
 #include "tree.cuh"
@@ -84,7 +83,8 @@ struct Joined {
         for (int e = 0; e < 8; ++e) o[e] *= inv;
     }
     // ... and adds the values that are not finite of the rows in `from` (at v, stride elements apart)
-    GPT_DEVINL void finish(unsigned long long from, const bf16* v, long long stride) {
+    template <typename E>
+    GPT_DEVINL void finish(unsigned long long from, const E* v, long long stride) {
         finish();
         for (; from; from &= from - 1) {
             float f[8];
@@ -623,223 +623,363 @@ __global__ void __launch_bounds__(THREADS, 2)
 }  // namespace tc
 
 // ---------------------------------------------------------------- fp32, head size 8 to 128
-// The same split in CUDA cores: tiles of 64 keys in shared memory; of the scores a thread has NB / 8 nodes
-// x 4 keys, of the values NB / 8 nodes x 4 G dimensions (NB: the nodes rounded up to 8, 16, 32 or 64;
-// G = 2 above head size 64).  Products are packed pairs of fp32 FMAs.  The next tile's K travels while the
-// values are summed, its V while the scores are.
-namespace simt {
-constexpr int THREADS = 128;
+// The same split with fp32 operands: every product of two fp32 numbers is taken as three TF32 products
+// (x = hi + lo, TF32 each; hi hi + hi lo + lo hi, fp32 accumulation), off by at most 5 x 2^-22 of it (the
+// product of the two lo, 2^-10 and 2^-11 of their numbers, and the roundings of each lo).
+//
+// Tiles of 64 keys come by TMA (panels of 32 dimensions, 128-byte swizzle), two in flight.  A warp has 16 of a
+// tile's keys and 16 MT nodes (NG groups of four warps take the nodes of up to 64): each K and V element is
+// read from shared memory once per group, the weights go from the scores' registers to the second product as
+// they are (the key order of its operands is chosen to match), and a warp keeps a softmax of its own, joined
+// at the end.
+//
+// Against CUDA-core tiles of 2 x 4 scores per thread, which shared-memory reads bind: 19 / 26 us (8 sequences
+// x 9 nodes x 12 heads of 64, up to 1013 keys), 63 / 84 us (32 x 30 x 12 of 64, 700 keys), 329 / 545 us
+// (20 x 50 x 16 of 128, 2000 keys).  The TF32 products bind it from about 32 nodes on (mma.sync: a 16 x 8 x 8
+// product took about 16 cycles per scheduler), their latency below.
+namespace f32 {
 constexpr int KEYS = 64;
+constexpr int STAGES = 2;
+// With one group a warp of its own issues the loads (a thousand cycles per tile); with two that ninth warp would
+// cost every thread a third of its registers, and thread 0 does it.
+constexpr int block_threads(int ng) { return ng == 1 ? 160 : 256; }
+constexpr int PANEL = KEYS * 128;   // bytes of 32 dimensions of a tile's rows
 
-GPT_DEVINL void cp_async16(void* dst, const void* src, int src_bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(src_bytes) : "memory");
-}
-GPT_DEVINL void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int PENDING> GPT_DEVINL void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory"); }
-
-constexpr int smem_floats(int nb, int hs) { return (nb + 2 * KEYS) * (hs + 4) + nb * (KEYS + 4); }
-
-GPT_DEVINL void lds_pairs(const float* p, uint64_t (&v)[2]) {
-    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(p);
-    v[0] = w.x, v[1] = w.y;
+template <int P, int MT, int NG>
+constexpr int smem_bytes() {
+    return 2 * STAGES * P * PANEL + P * 4 * MT * NG * 2 * 32 * 16 + 1024;
 }
 
-template <int NB, int G>
-__global__ void __launch_bounds__(THREADS)
-    tree_attention_f32(const float* __restrict__ qkv, const float* __restrict__ kv, float* __restrict__ y, const TreeArgs a) {
-    constexpr int RN = NB / 8;
-    extern __shared__ __align__(16) float sm[];
-    __shared__ unsigned long long see[kMaxNodes];
+GPT_DEVINL uint32_t tf32(float x) {
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+GPT_DEVINL void split(float x, uint32_t& hi, uint32_t& lo) {
+    hi = tf32(x);
+    lo = tf32(x - __uint_as_float(hi));
+}
+// K and V: hi cut, not rounded, so that the type's largest values stay finite (a masked one is multiplied by 0).
+GPT_DEVINL void split_cut(float x, uint32_t& hi, uint32_t& lo) {
+    hi = __float_as_uint(x) & 0xffffe000u;
+    lo = tf32(x - __uint_as_float(hi));
+}
+GPT_DEVINL void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm(
+        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The 16-byte piece `chunk` of a panel's row.
+GPT_DEVINL float4 piece(const uint8_t* panel, int row, int chunk) {
+    return *reinterpret_cast<const float4*>(panel + row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+template <int P, int MT, int NG>
+__global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 1 ? 2 : 3)
+    tree_attention_f32(const __grid_constant__ CUtensorMap tmNode, const __grid_constant__ CUtensorMap tmCache,
+                       const float* __restrict__ qkv, float* __restrict__ y, const TreeArgs a) {
+    constexpr int THREADS = 128 * NG, ROWS = 16 * MT * NG, LD = 32 * P + 4;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint4* sQ = reinterpret_cast<uint4*>(ring + 2 * STAGES * P * PANEL);   // [step][node tile][hi, lo][lane]
+    __shared__ unsigned long long see[kMaxNodes], s_bad;
+    __shared__ uint64_t full[STAGES], empty[STAGES];
     __shared__ int par[kMaxNodes];
-    __shared__ float2 ml[NB];
-    const int hs = a.hs, ld = hs + 4, N = a.N;
-    float* sQ = sm;
-    float* sK = sQ + NB * ld;
-    float* sV = sK + KEYS * ld;
-    float* sP = sV + KEYS * ld;
-    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    __shared__ float2 ml[ROWS];
+    __shared__ int s_abort;
+    volatile int* abort_flag = &s_abort;
+    const int hs = a.hs, N = a.N;
+    const int tid = threadIdx.x, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    const int key_warp = (tid >> 5) & 3, group = tid >> 7;
     const int rank = static_cast<int>(cluster_ctarank());
     const int pair = static_cast<int>(blockIdx.x) / a.cluster;
     const int b = pair / a.nh, h = pair - b * a.nh;
     const long long C = static_cast<long long>(a.nh) * hs;
     const float* node = qkv + static_cast<long long>(b) * N * 3 * C + h * hs;
-    const float* cache = kv + static_cast<long long>(b) * a.block_size * 2 * C + h * hs;
-    // rows are copied by 2^row_shift threads each, 16 bytes per thread
-    int row_shift = 1;
-    while (4 << row_shift < hs) ++row_shift;
-    const int row0 = tid >> row_shift, col = (tid & ((1 << row_shift) - 1)) * 4, row_step = THREADS >> row_shift;
-    // `rows` rows at src (stride elements apart) to dst [total][ld], zeros behind them
-    auto copy_rows = [&](float* dst, const float* src, long long stride, int rows, int total) {
-        if (col < hs)
-            for (int i = row0; i < total; i += row_step)
-                cp_async16(dst + i * ld + col, i < rows ? src + i * stride + col : node, i < rows ? 16 : 0);
-        cp_async_commit();
-    };
+    if (tid == 0) {
+        for (int st = 0; st < STAGES; ++st) mbar_init(&full[st], 1), mbar_init(&empty[st], 4 * NG);
+        s_abort = 0;
+        s_bad = 0;
+        fence_barrier_init();
+        fence_proxy_async_shared();
+        tma_prefetch_desc(&tmNode);
+        tma_prefetch_desc(&tmCache);
+    }
+    __syncthreads();
     griddep_launch_dependents();
     griddep_wait();
-    copy_rows(sQ, node, 3 * C, N, NB);
     const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && tid == 0 ? a.status : nullptr);
-    const int n_cache = (len + KEYS - 1) / KEYS;
-    auto copy_tile = [&](int t, int v) {
-        float* dst = v ? sV : sK;
-        if (t > n_cache) cp_async_commit();
-        else if (t == n_cache) copy_rows(dst, node + (1 + v) * C, 3 * C, N, KEYS);
-        else copy_rows(dst, cache + static_cast<long long>(t) * KEYS * 2 * C + v * C, 2 * C, len - t * KEYS, KEYS);
+    const int n_cache = (len + KEYS - 1) / KEYS;   // tile n_cache is the nodes'
+    const int n_panels = (hs + 31) / 32;
+    auto load_tile = [&](int t, int stage) {   // one thread
+        if (t > n_cache) return;
+        mbar_arrive_expect_tx(&full[stage], 2 * n_panels * PANEL);
+        for (int v = 0; v < 2; ++v)
+            for (int p = 0; p < n_panels; ++p) {
+                uint8_t* dst = ring + (2 * stage + v) * P * PANEL + p * PANEL;
+                if (t < n_cache) tma_load_4d(dst, &tmCache, &full[stage], 32 * p, v * a.nh + h, t * KEYS, b);
+                else tma_load_4d(dst, &tmNode, &full[stage], 32 * p, (1 + v) * a.nh + h, 0, b);
+            }
     };
-    copy_tile(rank, 0);
-    copy_tile(rank, 1);
+    constexpr int LOADER = NG == 1 ? THREADS : 0;   // the loading thread
+    if (tid == LOADER)
+        for (int st = 0; st < STAGES; ++st) load_tile(rank + st * a.cluster, st);
+
+    // The queries as operand fragments.  Step 2c + e of a chunk of 16 dimensions takes dimensions
+    // 16 c + 4 t + 2 e (k = t) and the next one (k = t + 4), so that a thread's K values are 16 bytes.
+    const int n_steps = 2 * ((hs + 15) / 16);
+    for (int it = tid; it < n_steps * MT * NG * 32; it += block_threads(NG)) {
+        const int l = it & 31, tile = (it >> 5) % (MT * NG), s = (it >> 5) / (MT * NG);
+        const int row = tile * 16 + (l >> 2), dim = (s >> 1) * 16 + (l & 3) * 4 + (s & 1) * 2;
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = row + (e & 1) * 8, d = dim + (e >> 1);
+            split(i < N && d < hs ? __ldcg(node + i * 3 * C + d) : 0.f, hi[e], lo[e]);
+        }
+        sQ[((s * MT * NG + tile) * 2) * 32 + l] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        sQ[((s * MT * NG + tile) * 2 + 1) * 32 + l] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
     load_tree(a, b, h == 0 && rank == 0, par, see);
 
-    uint64_t o[RN][2 * G];
-    float m[RN], l[RN];
+    float o[MT][P][4][4];
+    float m[MT][2], l[MT][2];   // of rows g and g + 8 of a node tile
+    unsigned long long sees[MT][2];
 #pragma unroll
-    for (int i = 0; i < RN; ++i) {
-        m[i] = -INFINITY, l[i] = 0.f;
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int d = 0; d < 2 * G; ++d) o[i][d] = 0;
+        for (int r = 0; r < 2; ++r) {
+            m[mt][r] = -INFINITY, l[mt][r] = 0.f;
+            sees[mt][r] = see[((group * MT + mt) * 16 + g + 8 * r) & (kMaxNodes - 1)];
+        }
+#pragma unroll
+        for (int p = 0; p < P; ++p)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][p][q][e] = 0.f;
     }
-    for (int t = rank; t <= n_cache; t += a.cluster) {
+    const int key0 = key_warp * 16;
+    bool ok = true;
+    int n = 0;   // tiles taken
+    if (tid >= THREADS) {
+        if (lane == 0) {
+            for (int t = rank; t <= n_cache; t += a.cluster, ++n) {
+                if (t + STAGES * a.cluster > n_cache) continue;
+                if (!(ok = mbar_wait(&empty[n % STAGES], (n / STAGES) & 1, abort_flag))) break;
+                load_tile(t + STAGES * a.cluster, n % STAGES);
+            }
+        }
+    } else for (int t = rank; t <= n_cache; t += a.cluster, ++n) {
+        const int stage = n % STAGES;
+        uint8_t* sK = ring + 2 * stage * P * PANEL;
+        uint8_t* sV = sK + P * PANEL;
         const bool nodes = t == n_cache;
         const int keys = nodes ? N : min(KEYS, len - t * KEYS);
-        cp_async_wait<1>();   // this tile's K (and the queries); its V may still travel
-        __syncthreads();
-        float s[RN][4];
-        {
-            uint64_t acc[RN][4];
+        ok = mbar_wait(&full[stage], (n / STAGES) & 1, abort_flag) && ok;
+        if (nodes || keys < KEYS) {
+            // V rows that must not matter are cleared; values of nodes that are not finite wait for the end
+            for (int it = tid; it < n_panels * KEYS * 8; it += THREADS) {
+                const int row = (it >> 3) & (KEYS - 1);
+                uint4* at = reinterpret_cast<uint4*>(sV + it * 16);
+                if (row >= keys || (nodes && see[row] == 0)) {
+                    *at = make_uint4(0, 0, 0, 0);
+                } else if (nodes) {
+                    uint32_t w[4] = {at->x, at->y, at->z, at->w};
+                    bool any = false;
 #pragma unroll
-            for (int i = 0; i < RN; ++i)
+                    for (int e = 0; e < 4; ++e)
+                        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] = 0, any = true;
+                    if (any) {
+                        *at = make_uint4(w[0], w[1], w[2], w[3]);
+                        atomicOr(&s_bad, 1ull << row);
+                    }
+                }
+            }
+            named_barrier(1, THREADS);
+        }
+        if (key0 < keys) {   // (warp-uniform)
+            // with one node tile by product, so that there are enough chains that do not wait for each other
+            float s[MT][2][4], s1[MT][2][4], s2[MT][2][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[i][k] = 0;
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[mt][j][e] = s1[mt][j][e] = s2[mt][j][e] = 0.f;
 #pragma unroll 2
-            for (int d = 0; d < hs; d += 4) {
-                uint64_t kk[4][2];
+            for (int c = 0; c < n_steps / 2; ++c) {
+                uint32_t bh[2][4], bl[2][4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) lds_pairs(sK + (tx + 16 * k) * ld + d, kk[k]);
-#pragma unroll
-                for (int i = 0; i < RN; ++i) {
-                    uint64_t q[2];
-                    lds_pairs(sQ + (ty * RN + i) * ld + d, q);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) acc[i][k] = f2_fma(q[1], kk[k][1], f2_fma(q[0], kk[k][0], acc[i][k]));
+                for (int j = 0; j < 2; ++j) {
+                    const float4 k = piece(sK + (c >> 1) * PANEL, key0 + 8 * j + g, (c & 1) * 4 + t4);
+                    split_cut(k.x, bh[j][0], bl[j][0]), split_cut(k.y, bh[j][1], bl[j][1]);
+                    split_cut(k.z, bh[j][2], bl[j][2]), split_cut(k.w, bh[j][3], bl[j][3]);
                 }
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint4* f = sQ + (((2 * c + e) * MT * NG + group * MT + mt) * 2) * 32 + lane;
+                        const uint4 fh = f[0], fl = f[32];
+                        const uint32_t ah[4] = {fh.x, fh.y, fh.z, fh.w}, al[4] = {fl.x, fl.y, fl.z, fl.w};
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            mma(MT == 1 ? s1[mt][j] : s[mt][j], al, bh[j][2 * e], bh[j][2 * e + 1]);
+                            mma(MT == 1 ? s2[mt][j] : s[mt][j], ah, bl[j][2 * e], bl[j][2 * e + 1]);
+                            mma(s[mt][j], ah, bh[j][2 * e], bh[j][2 * e + 1]);
+                        }
+                    }
             }
+            float x[MT][2][4], mx[MT][2];   // [row g, g + 8][key 2 t, 2 t + 1, the same + 8]
 #pragma unroll
-            for (int i = 0; i < RN; ++i)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float lo, hi;
-                    f2_unpack(acc[i][k], lo, hi);
-                    s[i][k] = lo + hi;
+                for (int r = 0; r < 2; ++r) {
+                    const uint32_t live = nodes ? static_cast<uint32_t>(sees[mt][r] >> key0) : keys - key0 >= 16 ? 0xffffu : (1u << (keys - key0)) - 1;
+                    mx[mt][r] = m[mt][r];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int j = e >> 1, c = 2 * r + (e & 1);
+                        const float v = s[mt][j][c] + (s1[mt][j][c] + s2[mt][j][c]);
+                        x[mt][r][e] = (live >> (8 * j + 2 * t4 + (e & 1))) & 1 ? v * a.scale_log2 : -INFINITY;
+                        mx[mt][r] = fmaxf(mx[mt][r], x[mt][r][e]);
+                    }
                 }
-        }
-        __syncthreads();
-        copy_tile(t + a.cluster, 0);
 #pragma unroll
-        for (int i = 0; i < RN; ++i) {
-            const unsigned long long mine = see[ty * RN + i];
-            float mx = -INFINITY;
+            for (int d = 1; d <= 2; ++d)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int key = tx + 16 * k;
-                const bool live = nodes ? (mine >> key) & 1 : key < keys;
-                s[i][k] = live ? s[i][k] * a.scale_log2 : -INFINITY;
-                mx = fmaxf(mx, s[i][k]);
-            }
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int x = 8; x > 0; x >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, x));
-            mx = fmaxf(mx, m[i]);
-            const float off = mx == -INFINITY ? 0.f : mx;
-            const float alpha = m[i] == mx ? 1.f : exp2_approx(m[i] - off);
-            m[i] = mx;
-            float sum = 0.f;
+                    for (int r = 0; r < 2; ++r) mx[mt][r] = fmaxf(mx[mt][r], __shfl_xor_sync(0xffffffffu, mx[mt][r], d));
+            uint32_t ph[MT][2][4], pl[MT][2][4];   // the weights as operands: {row g, g + 8} x {key 2 t, 2 t + 1}
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float p = exp2_approx(s[i][k] - off);
-                sP[(ty * RN + i) * (KEYS + 4) + tx + 16 * k] = p;
-                sum += p;
-            }
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-            for (int x = 8; x > 0; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-            l[i] = l[i] * alpha + sum;
+                for (int r = 0; r < 2; ++r) {
+                    const float off = mx[mt][r] == -INFINITY ? 0.f : mx[mt][r];
+                    const float alpha = m[mt][r] == mx[mt][r] ? 1.f : exp2_approx(m[mt][r] - off);
+                    m[mt][r] = mx[mt][r];
+                    l[mt][r] *= alpha;
 #pragma unroll
-            for (int d = 0; d < 2 * G; ++d) o[i][d] = f2_mul(o[i][d], f2_pack(alpha, alpha));
-        }
-        cp_async_wait<1>();   // this tile's V
-        __syncthreads();
-        auto sum_values = [&](auto is_nodes) {
-            unsigned long long mine[RN];
-            if (is_nodes) {
-#pragma unroll
-                for (int i = 0; i < RN; ++i) mine[i] = see[ty * RN + i];
-            }
-#pragma unroll 1
-            for (int k = 0; k < keys; k += 4) {   // (weights behind the last key are 0, V rows zeros)
-                float4 p[RN];
-#pragma unroll
-                for (int i = 0; i < RN; ++i) p[i] = *reinterpret_cast<const float4*>(sP + (ty * RN + i) * (KEYS + 4) + k);
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    uint64_t v[G][2];
-#pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        v[g][0] = v[g][1] = 0;
-                        if (tx * 4 + 64 * g < hs) lds_pairs(sV + (k + x) * ld + tx * 4 + 64 * g, v[g]);
+                    for (int e = 0; e < 4; ++e) {
+                        const float p = exp2_approx(x[mt][r][e] - off);
+                        l[mt][r] += p;
+                        split(p, ph[mt][e >> 1][r + 2 * (e & 1)], pl[mt][e >> 1][r + 2 * (e & 1)]);
                     }
 #pragma unroll
-                    for (int i = 0; i < RN; ++i) {
-                        // another branch's value may be NaN: it is not even multiplied by 0
-                        if (is_nodes && !((mine[i] >> (k + x)) & 1)) continue;
-                        const float w = x == 0 ? p[i].x : x == 1 ? p[i].y : x == 2 ? p[i].z : p[i].w;
-                        const uint64_t ww = f2_pack(w, w);
+                    for (int p = 0; p < P; ++p)
 #pragma unroll
-                        for (int g = 0; g < G; ++g) {
-                            o[i][2 * g] = f2_fma(ww, v[g][0], o[i][2 * g]);
-                            o[i][2 * g + 1] = f2_fma(ww, v[g][1], o[i][2 * g + 1]);
+                        for (int q = 0; q < 4; ++q) o[mt][p][q][2 * r] *= alpha, o[mt][p][q][2 * r + 1] *= alpha;
+                }
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+                if (p >= n_panels) break;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int row = key0 + 8 * j + 2 * t4;
+                    const float4 v0 = piece(sV + p * PANEL, row, g), v1 = piece(sV + p * PANEL, row + 1, g);
+                    const float x0[4] = {v0.x, v0.y, v0.z, v0.w}, x1[4] = {v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {   // dimensions 4 n + q of the panel
+                        uint32_t b0h, b0l, b1h, b1l;
+                        split_cut(x0[q], b0h, b0l), split_cut(x1[q], b1h, b1l);
+#pragma unroll
+                        for (int mt = 0; mt < MT; ++mt) {
+                            mma(o[mt][p][q], pl[mt][j], b0h, b1h);
+                            mma(o[mt][p][q], ph[mt][j], b0l, b1l);
+                            mma(o[mt][p][q], ph[mt][j], b0h, b1h);
                         }
                     }
                 }
             }
-        };
-        if (nodes) sum_values(std::true_type());
-        else sum_values(std::false_type());
+        }
+        fence_proxy_async_shared();   // what was read and cleared here before what the next copies write
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (NG > 1 && tid == LOADER && t + STAGES * a.cluster <= n_cache) {
+            ok = mbar_wait(&empty[stage], (n / STAGES) & 1, abort_flag) && ok;
+            if (ok) load_tile(t + STAGES * a.cluster, stage);
+        }
+        __syncwarp();
+    }
+    if (!ok) {   // no bulk copy may still target shared memory when the CTA exits
+        for (int i = 1; tid < THREADS && i <= STAGES && i <= n; ++i) mbar_drain(&full[(n - i) % STAGES], ((n - i) / STAGES) & 1);
+        set_status(a.status, GPT_ERR_TIMEOUT);
+    }
+    __syncthreads();
+
+    // The warps' parts joined one after another in the ring's place, then the CTAs'.
+    float* sO = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 1);
+            l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 2);
+        }
+    for (int w = 0; w < 4; ++w) {
+        if (key_warp == w && tid < THREADS) {
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const int i = (group * MT + mt) * 16 + g + 8 * r;
+                    const float2 old = w ? ml[i] : make_float2(-INFINITY, 0.f);
+                    const bool have_old = old.y != 0.f, have = l[mt][r] != 0.f;
+                    const float M = have_old ? have ? fmaxf(old.x, m[mt][r]) : old.x : m[mt][r];
+                    const float f_old = !have_old ? 0.f : old.x == M ? 1.f : exp2_approx(old.x - M);
+                    const float f = !have ? 0.f : m[mt][r] == M ? 1.f : exp2_approx(m[mt][r] - M);
+#pragma unroll
+                    for (int p = 0; p < P; ++p)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {   // four dimensions
+                            float4* at = reinterpret_cast<float4*>(sO + i * LD + p * 32 + 8 * t4 + 4 * e);
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (have_old) v = *at;
+                            if (have_old) v.x *= f_old, v.y *= f_old, v.z *= f_old, v.w *= f_old;
+                            if (have) {
+                                v.x = fmaf(f, o[mt][p][0][2 * r + e], v.x), v.y = fmaf(f, o[mt][p][1][2 * r + e], v.y);
+                                v.z = fmaf(f, o[mt][p][2][2 * r + e], v.z), v.w = fmaf(f, o[mt][p][3][2 * r + e], v.w);
+                            }
+                            *at = v;
+                        }
+                    __syncwarp();
+                    if (t4 == 0) ml[i] = make_float2(M, (have_old ? old.y * f_old : 0.f) + (have ? l[mt][r] * f : 0.f));
+                }
+        }
         __syncthreads();
-        copy_tile(t + a.cluster, 1);
     }
-    cp_async_wait<0>();
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < RN; ++i) {
-#pragma unroll
-        for (int g = 0; g < G; ++g)
-            if (tx * 4 + 64 * g < hs)
-                *reinterpret_cast<ulonglong2*>(sK + (ty * RN + i) * ld + tx * 4 + 64 * g) = make_ulonglong2(o[i][2 * g], o[i][2 * g + 1]);
-        if (tx == 0) ml[ty * RN + i] = make_float2(m[i], l[i]);
-    }
-    __syncthreads();
     cluster_sync();
-    join_cluster(sK, ld, ml, see, a, hs / 8, rank, y + static_cast<long long>(b) * N * C + h * hs, C,
-                 [](int, int, Joined& j) { j.finish(); });
+    const int holder = n_cache % a.cluster;   // of the nodes' tile
+    const unsigned long long bad =
+        static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&s_bad) + 1, holder))) << 32 |
+        ld_cluster_u32(map_to_rank(&s_bad, holder));
+    join_cluster(sO, LD, ml, see, a, hs / 8, rank, y + static_cast<long long>(b) * N * C + h * hs, C,
+                 [&](int i, int d, Joined& x) { x.finish(bad & see[i], node + 2 * C + d, 3 * C); });
     __syncwarp();
     cluster_sync();
 }
 
-template <int NB, int G>
-int launch(const void* qkv, const void* kv, void* y, const TreeArgs& a, unsigned ctas, cudaStream_t s) {
+template <int P, int MT, int NG>
+int launch(const CUtensorMap& node_map, const CUtensorMap& cache_map, const void* qkv, void* y, const TreeArgs& a,
+           unsigned ctas, cudaStream_t s) {
     static size_t opted[kMaxDevices] = {};
-    const size_t smem = sizeof(float) * smem_floats(NB, a.hs);
-    const int rc = opt_in_smem(reinterpret_cast<const void*>(tree_attention_f32<NB, G>), smem, opted);
+    const int rc = opt_in_smem(reinterpret_cast<const void*>(tree_attention_f32<P, MT, NG>), smem_bytes<P, MT, NG>(), opted);
     if (rc) return rc;
-    return launch_overlapped_cluster(tree_attention_f32<NB, G>, a.cluster, dim3(ctas), dim3(THREADS), smem, s,
-                                     static_cast<const float*>(qkv), static_cast<const float*>(kv), static_cast<float*>(y), a);
+    return launch_overlapped_cluster(tree_attention_f32<P, MT, NG>, a.cluster, dim3(ctas), dim3(block_threads(NG)),
+                                     smem_bytes<P, MT, NG>(), s, node_map, cache_map, static_cast<const float*>(qkv),
+                                     static_cast<float*>(y), a);
 }
-template <int G>
-int launch(const void* qkv, const void* kv, void* y, const TreeArgs& a, unsigned ctas, cudaStream_t s) {
-    if (a.N <= 8) return launch<8, G>(qkv, kv, y, a, ctas, s);
-    if (a.N <= 16) return launch<16, G>(qkv, kv, y, a, ctas, s);
-    if (a.N <= 32) return launch<32, G>(qkv, kv, y, a, ctas, s);
-    return launch<64, G>(qkv, kv, y, a, ctas, s);
+template <int P>
+int launch(const CUtensorMap& node_map, const CUtensorMap& cache_map, const void* qkv, void* y, const TreeArgs& a,
+           unsigned ctas, cudaStream_t s) {
+    if (a.N <= 16) return launch<P, 1, 1>(node_map, cache_map, qkv, y, a, ctas, s);
+    if (a.N <= 32) return launch<P, 2, 1>(node_map, cache_map, qkv, y, a, ctas, s);
+    return launch<P, 2, 2>(node_map, cache_map, qkv, y, a, ctas, s);
 }
-}  // namespace simt
+}  // namespace f32
 
 }  // namespace
 
@@ -855,28 +995,37 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
     a.block_size = block_size;
     a.scale_log2 = static_cast<float>(1.4426950408889634 / sqrt(static_cast<double>(hs)));
     a.status = status;
-    const bool f32 = dtype == GPT_DTYPE_F32;
+    const bool is_f32 = dtype == GPT_DTYPE_F32;
     const long long pairs = static_cast<long long>(B) * nh;
-    const int tiles = (block_size - 1) / (f32 ? simt::KEYS : tc::KEYS) + 2;
+    const int tiles = (block_size - 1) / (is_f32 ? f32::KEYS : tc::KEYS) + 2;
     a.cluster = 1;
-    const long long slots = 148 * (f32 ? 5 : 2);   // CTAs that run at a time
-    while (a.cluster < 8 && pairs * a.cluster * 2 <= slots && a.cluster < tiles) a.cluster *= 2;
+    // CTAs that run at a time
+    const long long slots = 148 * (!is_f32 ? 2 : hs > 64 || N > 32 ? 1 : N > 16 ? 2 : 3);
+    while (a.cluster < 8 && a.cluster < tiles &&
+           (pairs * a.cluster * 2 <= slots || (pairs * a.cluster * 2 <= 2 * slots && tiles >= 48 * a.cluster)))
+        a.cluster *= 2;
     // more CTAs than run at a time: those with the most work start first
-    a.longest_first = !f32 && B > 1 && B <= tc::THREADS && pairs * a.cluster > slots;
+    a.longest_first = !is_f32 && B > 1 && B <= tc::THREADS && pairs * a.cluster > slots;
     // bf16 without clusters: persistent CTAs
-    const dim3 grid(static_cast<unsigned>((f32 || a.cluster > 1 || pairs < slots ? pairs : slots) * a.cluster));
-    if (f32) return hs <= 64 ? simt::launch<1>(qkv, kv, y, a, grid.x, s) : simt::launch<2>(qkv, kv, y, a, grid.x, s);
-    int rc;
+    const dim3 grid(static_cast<unsigned>((is_f32 || a.cluster > 1 || pairs < slots ? pairs : slots) * a.cluster));
     // {hs, heads of q, k, v (nodes) or k, v (cache), rows, sequences}
-    const uint64_t C2 = static_cast<uint64_t>(nh) * hs * 2;
-    const uint64_t node_dims[4] = {64, static_cast<uint64_t>(3) * nh, static_cast<uint64_t>(N), static_cast<uint64_t>(B)};
-    const uint64_t node_strides[3] = {128, 3 * C2, 3 * C2 * N};
-    const uint32_t node_box[4] = {64, 1, tc::BOX, 1};
-    const uint64_t cache_dims[4] = {64, static_cast<uint64_t>(2) * nh, static_cast<uint64_t>(block_size), static_cast<uint64_t>(B)};
-    const uint64_t cache_strides[3] = {128, 2 * C2, 2 * C2 * block_size};
-    const uint32_t cache_box[4] = {64, 1, tc::KEYS, 1};
-    const uint32_t rest_box[4] = {64, 1, tc::BOX, 1};
+    const uint64_t heads = nh, row = heads * hs * (is_f32 ? 4 : 2), hs_bytes = row / heads;
+    const uint64_t node_dims[4] = {static_cast<uint64_t>(hs), 3 * heads, static_cast<uint64_t>(N), static_cast<uint64_t>(B)};
+    const uint64_t node_strides[3] = {hs_bytes, 3 * row, 3 * row * N};
+    const uint64_t cache_dims[4] = {static_cast<uint64_t>(hs), 2 * heads, static_cast<uint64_t>(block_size), static_cast<uint64_t>(B)};
+    const uint64_t cache_strides[3] = {hs_bytes, 2 * row, 2 * row * block_size};
     CUtensorMap node_map, cache_map, rest_map;
+    int rc;
+    if (is_f32) {
+        const uint32_t box[4] = {32, 1, f32::KEYS, 1};
+        rc = make_tmap_f32_4d(&node_map, qkv, node_dims, node_strides, box);
+        if (!rc) rc = make_tmap_f32_4d(&cache_map, kv, cache_dims, cache_strides, box);
+        if (rc) return rc;
+        return hs <= 32   ? f32::launch<1>(node_map, cache_map, qkv, y, a, grid.x, s)
+               : hs <= 64 ? f32::launch<2>(node_map, cache_map, qkv, y, a, grid.x, s)
+                          : f32::launch<4>(node_map, cache_map, qkv, y, a, grid.x, s);
+    }
+    const uint32_t node_box[4] = {64, 1, tc::BOX, 1}, cache_box[4] = {64, 1, tc::KEYS, 1}, rest_box[4] = {64, 1, tc::BOX, 1};
     rc = make_tmap_bf16_4d(&node_map, qkv, node_dims, node_strides, node_box);
     if (!rc) rc = make_tmap_bf16_4d(&cache_map, kv, cache_dims, cache_strides, cache_box);
     if (!rc) rc = make_tmap_bf16_4d(&rest_map, kv, cache_dims, cache_strides, rest_box);

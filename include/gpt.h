@@ -338,12 +338,14 @@ int gpt_generate(const gpt_config_t* cfg, const void* weights, const int64_t* id
 /* Attention of the nodes over the cache and their ancestors:
  *   y[b, i, h] = sum_j softmax_j(q[b, i, h] . k_j / sqrt(hs)) v_j,
  *   j over cached positions [0, lengths[b]) and A(i).
- * Rows with no node are written as zeros.  What a row does not see cannot change it: cached positions
+ * Rows with no node are written as zeros.  A visible k or v that is not finite leaves NaN or an infinity in
+ * what it reaches.  What a row does not see cannot change it: cached positions
  * from lengths[b] on and other branches' k and v may hold any value, NaN included.
  *   qkv     [B, N, 3, nh * hs]; kv [B, block_size, 2, nh * hs]; y [B, N, nh * hs] (no overlap with
  *           the inputs); all in `dtype`, 16-byte aligned.
  *   GPT_DTYPE_BF16: hs 64 (fp32 scores, statistics and sums; the probabilities are rounded to bf16 as
- *           operands of the product with v).  GPT_DTYPE_F32: hs % 8 == 0, hs <= 128, fp32 throughout.
+ *           operands of the product with v).  GPT_DTYPE_F32: hs % 8 == 0, hs <= 128 (every product of two
+ *           fp32 numbers to 5 x 2^-22 of it, as three TF32 products; fp32 sums).
  *   N = 1 with parent -1 is the attention of an ordinary decode step with a length per sequence.
  *   status  optional device int32 (NULL allowed), never cleared by the library.
  * No workspace; results are bit-reproducible. */

@@ -104,6 +104,24 @@ def test_decode_step_wait_limit_gives_timeout_then_recovers():
     assert torch.equal(runs[0], runs[1])
 
 
+def test_tree_attention_of_many_rounds_ends_after_a_timeout(short_waits):
+    """More sequences and heads than run at a time: a CTA's warps leave their rounds together."""
+    native = short_waits
+    qkv = torch.ones((64, 5, 3, 1024), dtype=torch.bfloat16, device="cuda")
+    kv = torch.ones((64, 300, 2, 1024), dtype=torch.bfloat16, device="cuda")
+    lens = torch.arange(64, dtype=torch.int32, device="cuda") * 4
+    par = torch.arange(-1, 4, dtype=torch.int32, device="cuda").repeat(64, 1)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.tree_attention(qkv, kv, lens, par, 16, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_ERR_TIMEOUT
+    native.set_wait_limit_ns(0)
+    st.zero_()
+    y = native.tree_attention(qkv, kv, lens, par, 16, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_OK and (y == 1).all()
+
+
 @pytest.mark.parametrize("N", [20, 64])
 def test_tree_attention_wait_limit_gives_timeout_then_recovers(short_waits, N):
     """Clusters of CTAs: every CTA gives up, and none leaves before the others have read its part."""

@@ -5,7 +5,8 @@ Tolerance of the attention, with u = 2^-24, a = sum_j p_j |v_j| of the exact pro
 D = max_j sum_d |q_d k_jd| / sqrt(hs): a score is off by at most (hs + 4) u D, its exponential's argument
 by 2 u more of the scores' spread (at most 2 D), the exponential by 4 u, and the sums of p and of p v by
 n u each, so y is off by 2 a ((hs + 8) u D + (n + 8) u).  bf16 rounds each p as an operand (a 2^-8 more;
-the sum of p may be taken before or after that rounding) and y itself (2^-8 |y|).
+the sum of p may be taken before or after that rounding) and y itself (2^-8 |y|).  fp32 takes each product
+as three TF32 products, 20 u of it more, in both places.
 """
 import ctypes
 
@@ -43,7 +44,8 @@ def attn_tol(qkv, kv, lens, nh, y, a, dtype):
         n = int(lens[b])
         k = np.nan_to_num(np.abs(np.concatenate([kv[b, :n, 0], qkv[b, :, 1]])), posinf=0.0)
         D = np.einsum("ihd,jhd->ihj", np.abs(qkv[b, :, 0]).reshape(N, nh, hs), k.reshape(-1, nh, hs)).max(2) / np.sqrt(hs)
-        rel = 2 * ((hs + 8) * U * D + (n + N + 8) * U)
+        tf32 = 20 if dtype == "f32" else 0
+        rel = 2 * ((hs + 8 + tf32) * U * D + (n + N + 8 + tf32) * U)
         tol[b] = (a[b].reshape(N, nh, hs) * rel[:, :, None]).reshape(N, C)
     if dtype == "bf16":
         tol += 2.0 ** -8 * a * 1.01 + 2.0 ** -8 * (np.abs(y) + tol)
@@ -410,3 +412,29 @@ def test_other_streams_and_graph_of_a_whole_step():
     torch.cuda.synchronize()
     for a, b, c in zip(eager, side, replayed):
         assert all(torch.equal(x, y) for x, y in zip(a, b)) and all(torch.equal(x, y) for x, y in zip(a, c))
+
+
+def test_model_calls():
+    """GPT.verify is tree_step, the likeliest token and tree_accept; GPT.score is the log probabilities of
+    the forward's logits."""
+    from decoder_only_transformer_causal_b200 import native
+    B, T0, N = 2, 10, 5
+    m, cfg, W64, prompt, kv = tree_model("tiny", None, B, T0)
+    par = torch.tensor([[-1, 0, 1, 0, 3]] * B, dtype=torch.int32, device="cuda")
+    tok = torch.randint(0, 65, (B, N), generator=torch.Generator().manual_seed(1)).cuda()
+    lens = torch.full((B,), T0, dtype=torch.int32, device="cuda")
+    kv2, tq = kv.clone(), native.alloc_tree_qkv(m.cfg, B, N)
+    logits = native.tree_step(m.cfg, m.weights, tok, par, lens, kv2, tq, m.workspace(B, N))
+    want = native.tree_accept(m.cfg, par, tok, logits.argmax(-1), lens, tq, kv2)
+    acc, chosen = m.verify(tok, par, lens, kv)
+    assert torch.equal(chosen, logits.argmax(-1))
+    assert all(torch.equal(a, b) for a, b in zip(acc, want)) and torch.equal(kv, kv2)
+
+    idx, tgt = seeded.make_tokens(3, 20, 65, seed=77, ignore_frac=0.2)
+    r = m.score(idx.cuda(), tgt.cuda(), k=4)
+    z = oracle.forward(W64, cfg, idx.numpy(), None if tgt is None else tgt.numpy())["logits"]
+    lp = z - np.log(np.exp(z - z.max(-1, keepdims=True)).sum(-1, keepdims=True)) - z.max(-1, keepdims=True)
+    ref = np.where(tgt.numpy() >= 0, np.take_along_axis(lp, np.maximum(tgt.numpy(), 0)[..., None], -1)[..., 0], 0)
+    # a log probability moves by at most twice what the logits do
+    assert max_abs(f64(r.logp), ref) <= 2 * F32_ATOL and r.top_ids.shape == (3, 20, 4)
+    assert max_abs(f64(r.entropy), -(np.exp(lp) * lp).sum(-1)) <= 2 * F32_ATOL * (1 + np.abs(lp).max())
