@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 // at the end.
 //
 // Against CUDA-core tiles of 2 x 4 scores per thread, which shared-memory reads bind: 19 / 26 us (8 sequences
-// x 9 nodes x 12 heads of 64, up to 1013 keys), 63 / 84 us (32 x 30 x 12 of 64, 700 keys), 329 / 545 us
+// x 9 nodes x 12 heads of 64, up to 1013 keys), 68 / 84 us (32 x 30 x 12 of 64, 700 keys), 352 / 545 us
 // (20 x 50 x 16 of 128, 2000 keys).  The TF32 products bind it from about 32 nodes on (mma.sync: a 16 x 8 x 8
 // product took about 16 cycles per scheduler), their latency below.
 namespace f32 {
@@ -800,14 +800,15 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
             named_barrier(1, THREADS);
         }
         if (key0 < keys) {   // (warp-uniform)
-            // with one node tile by product, so that there are enough chains that do not wait for each other
-            float s[MT][2][4], s1[MT][2][4], s2[MT][2][4];
+            // A product's accumulator is cut, not rounded, at every step: short chains of them (16 dimensions; a
+            // tile's keys) are summed by ordinary adds.
+            float s[MT][2][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) s[mt][j][e] = s1[mt][j][e] = s2[mt][j][e] = 0.f;
+                    for (int e = 0; e < 4; ++e) s[mt][j][e] = 0.f;
 #pragma unroll 2
             for (int c = 0; c < n_steps / 2; ++c) {
                 uint32_t bh[2][4], bl[2][4];
@@ -818,21 +819,29 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
                     split_cut(k.z, bh[j][2], bl[j][2]), split_cut(k.w, bh[j][3], bl[j][3]);
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
+                for (int mt = 0; mt < MT; ++mt) {
+                    const uint4* f = sQ + ((2 * c * MT * NG + group * MT + mt) * 2) * 32 + lane;
+                    const uint4* f1 = f + MT * NG * 2 * 32;
+                    const uint4 w[4] = {f[0], f[32], f1[0], f1[32]};
+                    const uint32_t ah[2][4] = {{w[0].x, w[0].y, w[0].z, w[0].w}, {w[2].x, w[2].y, w[2].z, w[2].w}};
+                    const uint32_t al[2][4] = {{w[1].x, w[1].y, w[1].z, w[1].w}, {w[3].x, w[3].y, w[3].z, w[3].w}};
+                    float big[2][4] = {}, small[2][4] = {};
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const uint4* f = sQ + (((2 * c + e) * MT * NG + group * MT + mt) * 2) * 32 + lane;
-                        const uint4 fh = f[0], fl = f[32];
-                        const uint32_t ah[4] = {fh.x, fh.y, fh.z, fh.w}, al[4] = {fl.x, fl.y, fl.z, fl.w};
+                    for (int e = 0; e < 2; ++e) {
 #pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            mma(MT == 1 ? s1[mt][j] : s[mt][j], al, bh[j][2 * e], bh[j][2 * e + 1]);
-                            mma(MT == 1 ? s2[mt][j] : s[mt][j], ah, bl[j][2 * e], bl[j][2 * e + 1]);
-                            mma(s[mt][j], ah, bh[j][2 * e], bh[j][2 * e + 1]);
-                        }
+                        for (int j = 0; j < 2; ++j) mma(small[j], al[e], bh[j][2 * e], bh[j][2 * e + 1]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) mma(big[j], ah[e], bh[j][2 * e], bh[j][2 * e + 1]);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) mma(small[j], ah[e], bl[j][2 * e], bl[j][2 * e + 1]);
                     }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) s[mt][j][e] += big[j][e] + small[j][e];
+                }
             }
-            float x[MT][2][4], mx[MT][2];   // [row g, g + 8][key 2 t, 2 t + 1, the same + 8]
+            float x[MT][2][4], mx[MT][2], alpha[MT][2];   // [row g, g + 8][key 2 t, 2 t + 1, the same + 8]
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -842,8 +851,7 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int j = e >> 1, c = 2 * r + (e & 1);
-                        const float v = s[mt][j][c] + (s1[mt][j][c] + s2[mt][j][c]);
-                        x[mt][r][e] = (live >> (8 * j + 2 * t4 + (e & 1))) & 1 ? v * a.scale_log2 : -INFINITY;
+                        x[mt][r][e] = (live >> (8 * j + 2 * t4 + (e & 1))) & 1 ? s[mt][j][c] * a.scale_log2 : -INFINITY;
                         mx[mt][r] = fmaxf(mx[mt][r], x[mt][r][e]);
                     }
                 }
@@ -859,23 +867,20 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const float off = mx[mt][r] == -INFINITY ? 0.f : mx[mt][r];
-                    const float alpha = m[mt][r] == mx[mt][r] ? 1.f : exp2_approx(m[mt][r] - off);
+                    alpha[mt][r] = m[mt][r] == mx[mt][r] ? 1.f : exp2_approx(m[mt][r] - off);
                     m[mt][r] = mx[mt][r];
-                    l[mt][r] *= alpha;
+                    l[mt][r] *= alpha[mt][r];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float p = exp2_approx(x[mt][r][e] - off);
                         l[mt][r] += p;
                         split(p, ph[mt][e >> 1][r + 2 * (e & 1)], pl[mt][e >> 1][r + 2 * (e & 1)]);
                     }
-#pragma unroll
-                    for (int p = 0; p < P; ++p)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) o[mt][p][q][2 * r] *= alpha, o[mt][p][q][2 * r + 1] *= alpha;
                 }
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 if (p >= n_panels) break;
+                float tile[MT][4][4] = {};
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int row = key0 + 8 * j + 2 * t4;
@@ -887,12 +892,18 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
                         split_cut(x0[q], b0h, b0l), split_cut(x1[q], b1h, b1l);
 #pragma unroll
                         for (int mt = 0; mt < MT; ++mt) {
-                            mma(o[mt][p][q], pl[mt][j], b0h, b1h);
-                            mma(o[mt][p][q], ph[mt][j], b0l, b1l);
-                            mma(o[mt][p][q], ph[mt][j], b0h, b1h);
+                            mma(tile[mt][q], pl[mt][j], b0h, b1h);
+                            mma(tile[mt][q], ph[mt][j], b0l, b1l);
+                            mma(tile[mt][q], ph[mt][j], b0h, b1h);
                         }
                     }
                 }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[mt][p][q][e] = fmaf(o[mt][p][q][e], alpha[mt][e >> 1], tile[mt][q][e]);
             }
         }
         fence_proxy_async_shared();   // what was read and cleared here before what the next copies write

@@ -627,13 +627,16 @@ def tree_accept(cfg: GPTConfig, parents: torch.Tensor, tok: torch.Tensor, chosen
     if out is None:
         out = TreeAccept(torch.empty_like(parents), torch.empty_like(lengths), torch.empty(B, dtype=i64, device=dev),
                          torch.empty_like(lengths))
+        outs = [t.data_ptr() for t in out]
+    else:
+        outs = (_arg("path", out.path, i32, (B, N), dev), _arg("n_accepted", out.n_accepted, i32, (B,), dev),
+                _arg("next_token", out.next_token, i64, (B,), dev), _arg("lengths_out", out.lengths, i32, (B,), dev))
     _launch("gpt_tree_accept", index, kept.ref, _arg("parents", parents, i32, (B, N), dev),
             _arg("tok", tok, i64, (B, N), dev), _arg("chosen", chosen, i64, (B, N), dev),
             _arg("lengths", lengths, i32, (B,), dev), B, N,
             _arg("tree_qkv", tree_qkv, kept.dtype, (cfg.n_layer, B, N, 3, cfg.n_embd), dev),
-            _buffer("kv_cache", kv_cache, B * kept.kv_bytes, dev), _arg("path", out.path, i32, (B, N), dev),
-            _arg("n_accepted", out.n_accepted, i32, (B,), dev), _arg("next_token", out.next_token, i64, (B,), dev),
-            _arg("lengths_out", out.lengths, i32, (B,), dev), _status_arg(status, dev), _stream_of(index, stream))
+            _buffer("kv_cache", kv_cache, B * kept.kv_bytes, dev), *outs, _status_arg(status, dev),
+            _stream_of(index, stream))
     return out
 
 
@@ -672,20 +675,25 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, k: 
     index, dev, f32, i64 = _cuda_index(logits), logits.device, torch.float32, torch.int64
     if out is None:
         logp, entropy, lse = torch.empty(3, rows, dtype=f32, device=dev).unbind(0)
-        out = TokenLogprobs(logp if tokens is not None else None, entropy, lse,
-                            torch.empty(rows, k, dtype=i64, device=dev) if k else None,
-                            torch.empty(rows, k, dtype=f32, device=dev) if k else None)
-    if rows:
+        if tokens is None:
+            logp = None
+        ids = top = None
+        if k > 0:
+            ids, top = torch.empty(rows, k, dtype=i64, device=dev), torch.empty(rows, k, dtype=f32, device=dev)
+        out = TokenLogprobs(logp, entropy, lse, ids, top)
+        outs = [None if t is None else t.data_ptr() for t in out]
+    else:
         logp, entropy, lse, ids, top = out
+        outs = [None if logp is None else _arg("logp", logp, f32, (rows,), dev),
+                None if entropy is None else _arg("entropy", entropy, f32, (rows,), dev),
+                None if lse is None else _arg("lse", lse, f32, (rows,), dev),
+                None if ids is None else _arg("top_ids", ids, i64, (rows, k), dev),
+                None if top is None else _arg("top_logp", top, f32, (rows, k), dev)]
+    if rows:
         _launch("gpt_token_logprobs", index, ptr, ld,
                 None if tokens is None else _arg("tokens", tokens, i64, (rows,), dev), rows, V,
-                _STORED[logits.dtype], float(temperature),
-                None if logp is None else _arg("logp", logp, f32, (rows,), dev),
-                None if entropy is None else _arg("entropy", entropy, f32, (rows,), dev),
-                None if lse is None else _arg("lse", lse, f32, (rows,), dev), int(k),
-                None if ids is None else _arg("top_ids", ids, i64, (rows, k), dev),
-                None if top is None else _arg("top_logp", top, f32, (rows, k), dev),
-                _status_arg(status, dev), _stream_of(index, stream))
+                _STORED[logits.dtype], float(temperature), *outs[:3], int(k), *outs[3:], _status_arg(status, dev),
+                _stream_of(index, stream))
     return out
 
 
