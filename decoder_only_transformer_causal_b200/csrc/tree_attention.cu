@@ -171,7 +171,7 @@ constexpr uint32_t TMEM_COLS = 256, COL_S = 0, COL_P = 128, COL_O = 192;
 constexpr float kRescaleThreshold = 8.f;      // as in the causal kernel: P stays below 2^8
 
 struct Tail {
-    uint64_t q_full, q_empty, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_full, s_free, p_full, o_done, drain;
+    uint64_t q_full, q_empty, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_free, p_full, drain;
     unsigned long long see[kMaxNodes], bad;   // bad: node rows of V with values that are not finite
     float2 ml[KEYS], joined_ml[kMaxNodes];
     int par[kMaxNodes];
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(THREADS, 2)
 
     if (threadIdx.x == 0) {
         uint64_t* bars = &T.q_full;
-        constexpr int n_bars = 2 + 4 * STAGES + 5;
+        constexpr int n_bars = 2 + 4 * STAGES + 3;
         for (int i = 0; i < n_bars; ++i) mbar_init(&bars[i], (&bars[i] == &T.s_free || &bars[i] == &T.p_full) ? 128u : 1u);
         T.abort = 0;
         T.bad = 0;
@@ -332,24 +332,22 @@ __global__ void __launch_bounds__(THREADS, 2)
         constexpr uint32_t idesc_s = make_idesc_bf16(128, KEYS, false), idesc_o = make_idesc_bf16(128, HS, true);
         const uint32_t tS = tmem + COL_S, tP = tmem + COL_P, tO = tmem + COL_O;
         const uint32_t q_addr = smem_addr(sQ), k_addr = smem_addr(sK), v_addr = smem_addr(sV);
-        auto wait = [&](uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag)) != 0;
-        };
+        auto wait = [&](uint64_t* bar, uint32_t parity) { return mbar_wait(bar, parity, abort_flag); };
+        auto all = [](bool v) { return __all_sync(0xffffffffu, v) != 0; };
         // Testing aid (gpt_set_wait_limit_ns): nothing arrives on `drain` before the commit below.
-        if (g_force_timeout) wait(&T.drain, 0);
+        if (g_force_timeout) all(wait(&T.drain, 0));
         bool ok = !g_force_timeout;
         int n = 0, n_q = 0;
         bool first = true;   // step n - 1 was its pair's first
         auto values = [&]() {   // O (+)= P_{n-1} V_{n-1}, once the softmax has written P_{n-1}
             const int st = (n - 1) % STAGES;
-            if (!wait(&T.p_full, (n - 1) & 1) || !wait(&T.v_full[st], ((n - 1) / STAGES) & 1)) return false;
+            if (!all(wait(&T.p_full, (n - 1) & 1) && wait(&T.v_full[st], ((n - 1) / STAGES) & 1))) return false;
             tc_fence_after();
             if (elect_one()) {
 #pragma unroll
                 for (int kk = 0; kk < KEYS / 16; ++kk)
                     umma_ts(tO, tP + kk * 8, make_sdesc_sw128(v_addr + st * TILE + kk * 2048), idesc_o, !first || kk > 0);
                 umma_commit(&T.v_empty[st]);
-                umma_commit(&T.o_done);
             }
             __syncwarp();
             return true;
@@ -359,11 +357,12 @@ __global__ void __launch_bounds__(THREADS, 2)
             for (int j = 0; j < w.n_steps; ++j, ++n) {
                 // between pairs the values first: the softmax waits for them, not for the next scores
                 if (j == 0 && n > 0 && !(ok = values())) break;
-                if (j == 0 && !(ok = wait(&T.q_full, n_q++ & 1))) break;
                 const int st = n % STAGES;
                 // S_n, once the softmax has taken S_{n-1} out of TMEM
-                if (!(ok = wait(&T.k_full[st], (n / STAGES) & 1))) break;
-                if (n > 0 && !(ok = wait(&T.s_free, (n - 1) & 1))) break;
+                ok = all((j > 0 || wait(&T.q_full, n_q & 1)) && wait(&T.k_full[st], (n / STAGES) & 1) &&
+                         (n == 0 || wait(&T.s_free, (n - 1) & 1)));
+                if (!ok) break;
+                n_q += j == 0;
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
@@ -371,7 +370,6 @@ __global__ void __launch_bounds__(THREADS, 2)
                         umma_ss(tS, make_sdesc_sw128(q_addr + kk * 32), make_sdesc_sw128(k_addr + st * TILE + kk * 32), idesc_s, kk > 0);
                     umma_commit(&T.k_empty[st]);
                     if (j == w.n_steps - 1) umma_commit(&T.q_empty);
-                    umma_commit(&T.s_full);
                 }
                 __syncwarp();
                 if (j > 0 && !(ok = values())) break;
@@ -454,7 +452,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     }
                     fence_proxy_async_shared();
                 }
-                const bool got = mbar_wait(&T.s_full, n & 1, abort_flag);
+                const bool got = mbar_wait(&T.k_empty[st], (n / STAGES) & 1, abort_flag);   // K_n read: S_n is there
                 __syncwarp();   // tcgen05.ld / st are warp-collective
                 if (!__all_sync(0xffffffffu, got)) {
                     ok = false;
@@ -507,7 +505,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 // P_n may overwrite P_{n-1} and O may be rescaled only after O += P_{n-1} V_{n-1} (for a
                 // pair's first step the join before it has waited for that).
                 if (j > 0) {
-                    const bool done = mbar_wait(&T.o_done, (n - 1) & 1, abort_flag);
+                    const bool done = mbar_wait(&T.v_empty[(n - 1) % STAGES], ((n - 1) / STAGES) & 1, abort_flag);
                     __syncwarp();
                     if (!__all_sync(0xffffffffu, done)) {
                         ok = false;
@@ -533,7 +531,7 @@ __global__ void __launch_bounds__(THREADS, 2)
             look_ahead(round + 1);
             bool have = false;
             if (ok && w.n_steps > 0) {
-                const bool done = mbar_wait(&T.o_done, (n - 1) & 1, abort_flag);
+                const bool done = mbar_wait(&T.v_empty[(n - 1) % STAGES], ((n - 1) / STAGES) & 1, abort_flag);
                 __syncwarp();
                 ok = have = __all_sync(0xffffffffu, done);
                 tc_fence_after();
