@@ -13,7 +13,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kUnrollLog2 = 2;
 constexpr int kUnroll = 1 << kUnrollLog2;   // 16-byte loads in flight per thread
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 constexpr int kCandidates = 512;    // places for the values at or above a part's top-k bound
 constexpr int kHits = 512;          // places for the steps that reach the bound
 constexpr int kSlots = 64;          // places per thread for the maxima of its steps (of kUnroll loads)
@@ -195,7 +195,10 @@ struct ScoreArgs {
     int32_t* status;
 };
 
-// A row is read once from HBM by a cluster of 1 to 8 CTAs, 16 bytes per load.
+// A row is read once from HBM by a cluster of 1, 2 or 4 CTAs, 16 bytes per load.  128 threads per row, eight
+// rows per SM: with 256 threads the ends of the rows (reductions, the list) left the memory idle (228 us
+// against 206 without a list); two steps in flight per thread cost a quarter of the threads and were slower
+// (313 against 265 us with 20 entries), as was asking L2 for the next row (325 against 228).
 //
 // Sums.  Each thread keeps a running maximum, raised once per 64 bytes, and the sums relative to it; the
 // threads' and then the CTAs' sums are joined in a fixed order.  Values are first raised to floor_z, so
@@ -206,20 +209,20 @@ struct ScoreArgs {
 // Top list.  The k-th largest of the CTA's thread maxima is a bound that at least k of its values
 // reach, and hardly more do: only the steps whose maximum reaches it (about k of them) are read
 // again, from L2.  More than 512 such values (long ties): a bisection over (value, index) finds a bound
-// that between k and 512 reach.  The values' ranks among the candidates, and across CTAs by binary
+// that between k and 512 reach.  12288 rows x 50257 bf16: 198 us without a list (6.2 TB/s), 224 with one
+// entry, 236 with 20, 264 with 64.  The values' ranks among the candidates, and across CTAs by binary
 // search in the others' lists, are their places in the list.
 template <typename E, int NT>
 __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
     griddep_launch_dependents();
     __shared__ float red[NT / 32], red_s[NT / 32], red_t[NT / 32];
     __shared__ int ired[NT / 32];
-    __shared__ unsigned long long cand[kCandidates];
+    __shared__ __align__(16) unsigned long long cand[kCandidates];
     __shared__ unsigned long long lists[NT == 128 ? 1 : kMaxCluster][GPT_TOP_MAX];
     __shared__ Part parts[kMaxCluster];
     __shared__ uint16_t slots[kSlots][NT], keys[NT];
     __shared__ uint32_t hits[kHits];
-    __shared__ uint32_t s_bound, s_hits;
-    __shared__ int s_count;
+    __shared__ uint32_t s_bound, s_hits, s_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int ncta = NT == 128 ? 1 : a.cluster;   // (known to the compiler for CTAs that are alone)
     const int rank = ncta > 1 ? static_cast<int>(cluster_ctarank()) : 0;
@@ -299,20 +302,26 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
     }
     if (a.k > 0 && warp == 0) {
         // the upper 16 bits of the k-th largest key, two bits at a time (three counts of at most 256 in one
-        // sum); 0 (every value) when fewer than k threads hold a value above floor_z
+        // sum): mostly it lies within 255 of the largest, else anywhere; 0 (every value) when fewer than k
+        // threads hold a value above floor_z
         uint32_t mine[NT / 32];
 #pragma unroll
         for (int j = 0; j < NT / 32; ++j) mine[j] = keys[j * 32 + lane];
-        uint32_t bound = 0;
+        const uint32_t k = a.k, top = key16(m);
+        uint32_t near = top > 255 ? top - 255 : 0;
+        int reach = 0;
 #pragma unroll
-        for (int bit = 14; bit >= 0; bit -= 2) {
-            const uint32_t b1 = bound | 1u << bit, b2 = bound | 2u << bit, b3 = bound | 3u << bit;
+        for (int j = 0; j < NT / 32; ++j) reach += mine[j] >= near;
+        int bit = 6;
+        if (static_cast<uint32_t>(__reduce_add_sync(0xffffffffu, reach)) < k) near = 0, bit = 14;
+        uint32_t bound = near;
+        for (; bit >= 0; bit -= 2) {
+            const uint32_t b1 = bound + (1u << bit), b2 = bound + (2u << bit), b3 = bound + (3u << bit);
             uint32_t above = 0;
 #pragma unroll
             for (int j = 0; j < NT / 32; ++j)
                 above += (mine[j] >= b1 ? 1u : 0u) + (mine[j] >= b2 ? 1u << 10 : 0u) + (mine[j] >= b3 ? 1u << 20 : 0u);
             above = __reduce_add_sync(0xffffffffu, above);
-            const uint32_t k = a.k;
             bound = above >> 20 >= k ? b3 : (above >> 10 & 1023u) >= k ? b2 : (above & 1023u) >= k ? b1 : bound;
         }
         if (lane == 0) s_bound = bound <= key16(a.floor_z) ? 0 : bound;
@@ -345,40 +354,75 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
     if (a.k > 0) {
         const uint32_t bound16 = s_bound;
         const float bound = bound16 == 0 ? -INFINITY : bound16 == 0xffffu ? INFINITY : key_value(bound16 << 16);
-        auto push = [&](float z, uint32_t col) {
-            const int at = atomicAdd(&s_count, 1);
-            if (at < kCandidates) cand[at] = entry(z, col);
-        };
-        if (my_key >= bound16) {   // this thread's steps that reach the bound
-            unsigned long long in = 0;   // (at most 64 slots)
-            const uint32_t n = (step + (1u << a.slot_shift) - 1) >> a.slot_shift;
-#pragma unroll 4
-            for (uint32_t j = 0; j < n; ++j) in |= static_cast<unsigned long long>(!(slot_value(slots[j][tid]) < bound)) << j;
-            for (; in; in &= in - 1) {
-                const uint32_t at = atomicAdd(&s_hits, 1u);
-                if (at < kHits) hits[at] = static_cast<uint32_t>(__ffsll(in) - 1) << 16 | tid;
+        // places for n entries of each lane, one addition to the counter per warp
+        auto reserve = [&](uint32_t n, uint32_t* counter) {
+            uint32_t upto = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+                if (lane >= o) upto += v;
             }
-            if (first < row.ends && !(z_end < bound)) push(z_end, row.end_col(first));
+            uint32_t base = 0;
+            if (lane == 31 && upto > 0) base = atomicAdd(counter, upto);
+            return __shfl_sync(0xffffffffu, base, 31) + upto - n;
+        };
+        {   // this thread's steps that reach the bound (at most 64 slots), and its element outside the units
+            unsigned long long in = 0;
+            uint32_t end = 0;
+            if (my_key >= bound16) {
+                const uint32_t n = (step + (1u << a.slot_shift) - 1) >> a.slot_shift;
+#pragma unroll 8
+                for (uint32_t j = 0; j < n; ++j) in |= static_cast<unsigned long long>(!(slot_value(slots[j][tid]) < bound)) << j;
+                end = first < row.ends && !(z_end < bound);
+            }
+            uint32_t at = reserve(__popcll(in), &s_hits);
+            for (; in; in &= in - 1, ++at)
+                if (at < kHits) hits[at] = static_cast<uint32_t>(__ffsll(in) - 1) << 16 | tid;
+            if (warp == 0) {   // (the elements outside the units are the first threads')
+                at = reserve(end, &s_count);
+                if (end && at < kCandidates) cand[at] = entry(z_end, row.end_col(first));
+            }
         }
         __syncthreads();
         const uint32_t n_hits = s_hits, each_log2 = kUnrollLog2 + a.slot_shift;
         if (n_hits <= kHits)
-            for (uint32_t i = tid; i < n_hits << each_log2; i += NT) {   // a unit each
-                const uint32_t hit = hits[i >> each_log2];
-                const uint32_t u = rank * NT + (hit & 0xffffu) + (((hit >> 16) << each_log2) + (i & ((1u << each_log2) - 1))) * row.stride;
-                if (u >= row.units) continue;
-                const uint4 w = __ldcg(reinterpret_cast<const uint4*>(row.z + row.unit_col(u)));
-                const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-                uint32_t in = 0, e = 0;
-                row.values(w, 0, [&](float z, uint32_t) { in |= static_cast<uint32_t>(!(z < bound)) << e++; });
-                for (; in; in &= in - 1) {
-                    const uint32_t at = __ffs(in) - 1, pos = sizeof(E) == 4 ? at : at >> 1;
-                    const uint32_t bits = pos == 0 ? x[0] : pos == 1 ? x[1] : pos == 2 ? x[2] : x[3];
-                    push(__uint_as_float(sizeof(E) == 4 ? bits : (at & 1) ? bits & 0xffff0000u : bits << 16), row.unit_col(u) + at);
+            for (uint32_t i0 = warp * 32; i0 < n_hits << each_log2; i0 += 4 * NT) {   // four units per lane at a time
+                uint4 w[4];
+                uint32_t cols[4], in[4], n = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const uint32_t i = i0 + x * NT + lane;
+                    cols[x] = 0xffffffffu;
+                    if (i < n_hits << each_log2) {
+                        const uint32_t hit = hits[i >> each_log2];
+                        const uint32_t u = rank * NT + (hit & 0xffffu) + (((hit >> 16) << each_log2) + (i & ((1u << each_log2) - 1))) * row.stride;
+                        if (u < row.units) {
+                            cols[x] = row.unit_col(u);
+                            w[x] = __ldcg(reinterpret_cast<const uint4*>(row.z + cols[x]));
+                        }
+                    }
                 }
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    in[x] = 0;
+                    if (cols[x] != 0xffffffffu) {
+                        uint32_t e = 0;
+                        row.values(w[x], 0, [&](float z, uint32_t) { in[x] |= static_cast<uint32_t>(!(z < bound)) << e++; });
+                    }
+                    n += __popc(in[x]);
+                }
+                uint32_t at = reserve(n, &s_count);
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    for (; in[x]; in[x] &= in[x] - 1, ++at) {
+                        const uint32_t e = __ffs(in[x]) - 1, pos = sizeof(E) == 4 ? e : e >> 1;
+                        const uint32_t bits = pos == 0 ? w[x].x : pos == 1 ? w[x].y : pos == 2 ? w[x].z : w[x].w;
+                        const float z = __uint_as_float(sizeof(E) == 4 ? bits : (e & 1) ? bits & 0xffff0000u : bits << 16);
+                        if (at < kCandidates) cand[at] = entry(z, cols[x] + e);
+                    }
             }
         __syncthreads();
-        int count = s_count;
+        uint32_t count = s_count;
         if (count > kCandidates || n_hits > kHits) {
             // the largest bound over (value, index) that at least k entries reach, bit by bit until few do
             unsigned long long at_least = 0;
@@ -397,22 +441,28 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
             __syncthreads();
             row.each(first, [&](float z, uint32_t col) {
                 const unsigned long long e = entry(z, col);
-                if (e >= at_least) cand[atomicAdd(&s_count, 1)] = e;
+                if (e >= at_least) cand[atomicAdd(&s_count, 1u)] = e;
             });
             __syncthreads();
             count = s_count;
         }
-        // places by counting: 8 lanes per candidate
-        for (int i0 = 0; i0 < count; i0 += NT / 8) {
-            const int i = i0 + (tid >> 3);
-            const unsigned long long e = i < count ? cand[i] : 0;
+        // places by counting
+        const uint32_t padded = (count + 7) & ~7u;   // (at most kCandidates)
+        if (tid < padded - count) cand[count + tid] = 0;
+        __syncthreads();
+        for (uint32_t i = tid; i < count; i += NT) {
+            const unsigned long long e = cand[i];
             int place = 0;
-            for (int j = tid & 7; j < count; j += 8) place += cand[j] > e;
+            for (uint32_t j = 0; j < padded; j += 8) {
+                ulonglong2 c[4];
 #pragma unroll
-            for (int o = 4; o > 0; o >>= 1) place += __shfl_xor_sync(0xffffffffu, place, o);
-            if (i < count && (tid & 7) == 0 && place < a.k) list[place] = e;
+                for (int x = 0; x < 4; ++x) c[x] = *reinterpret_cast<const ulonglong2*>(&cand[j + 2 * x]);
+#pragma unroll
+                for (int x = 0; x < 4; ++x) place += (c[x].x > e) + (c[x].y > e);
+            }
+            if (place < a.k) list[place] = e;
         }
-        if (tid >= count && tid < a.k) list[tid] = 0;   // a part shorter than k
+        if (tid >= static_cast<int>(count) && tid < a.k) list[tid] = 0;   // a part shorter than k
         __syncthreads();
     }
     if (ncta > 1) {
@@ -635,8 +685,11 @@ int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int
     a.top_ids = top_ids;
     a.top_logp = top_logp;
     a.status = status;
+    // Rows are split only while that leaves SMs without a CTA, and not below 2048 columns: joining the parts'
+    // lists costs more than it saves (64 rows x 50304 bf16, 64 alternatives: 2 CTAs a row 10.8,
+    // 4: 12.3, 8: 22.5 us; 8 rows fp32: 2: 11.8, 4: 11.3, 8: 15.4 us).
     int cluster = kMaxCluster;
-    while (cluster > 1 && (static_cast<long long>(rows) * cluster > 148 * 8 || V < cluster * 2048)) cluster /= 2;
+    while (cluster > 1 && (static_cast<long long>(rows) * cluster > 148 || V < cluster * 2048)) cluster /= 2;
     a.cluster = cluster;
     const long long step = static_cast<long long>(cluster > 1 ? 256 : 128) * cluster * kUnroll * (dtype == GPT_DTYPE_BF16 ? 8 : 4);
     while ((V + step - 1) / step > static_cast<long long>(kSlots) << a.slot_shift) ++a.slot_shift;
