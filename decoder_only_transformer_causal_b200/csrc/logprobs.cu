@@ -16,7 +16,7 @@ constexpr int kUnroll = 1 << kUnrollLog2;   // 16-byte loads in flight per threa
 constexpr int kMaxCluster = 4;
 constexpr int kCandidates = 512;    // places for the values at or above a part's top-k bound
 constexpr int kHits = 512;          // places for the steps that reach the bound
-constexpr int kSlots = 64;          // places per thread for the maxima of its steps (of kUnroll loads)
+constexpr int kSlots = 32;          // places per thread for the maxima of its steps (of kUnroll loads)
 
 template <typename E> constexpr int kVec = 16 / sizeof(E);
 
@@ -184,7 +184,7 @@ struct ScoreArgs {
     long long ld;
     const int64_t* tokens;
     uint32_t V;
-    int cluster;
+    int cluster, threads;
     float c, floor_z;        // log2(e) / T; the value that stands for everything at or below it
     uint32_t floor2;         // floor_z as a pair of bf16
     float *logp, *entropy, *lse;
@@ -195,9 +195,9 @@ struct ScoreArgs {
     int32_t* status;
 };
 
-// A row is read once from HBM by a cluster of 1, 2 or 4 CTAs, 16 bytes per load.  128 threads per row, eight
-// rows per SM: with 256 threads the ends of the rows (reductions, the list) left the memory idle (228 us
-// against 206 without a list); two steps in flight per thread cost a quarter of the threads and were slower
+// A row is read once from HBM by a cluster of 1, 2 or 4 CTAs, 16 bytes per load.  Many rows: 128 threads
+// each, nine (bf16) or eight (fp32) rows per SM: with 256 threads the ends of the rows (reductions, the list)
+// left the memory idle (228 us against 206 without a list); two steps in flight per thread cost a quarter of the threads and were slower
 // (313 against 265 us with 20 entries), as was asking L2 for the next row (325 against 228).
 //
 // Sums.  Each thread keeps a running maximum, raised once per 64 bytes, and the sums relative to it; the
@@ -209,11 +209,11 @@ struct ScoreArgs {
 // Top list.  The k-th largest of the CTA's thread maxima is a bound that at least k of its values
 // reach, and hardly more do: only the steps whose maximum reaches it (about k of them) are read
 // again, from L2.  More than 512 such values (long ties): a bisection over (value, index) finds a bound
-// that between k and 512 reach.  12288 rows x 50257 bf16: 198 us without a list (6.2 TB/s), 224 with one
-// entry, 236 with 20, 264 with 64.  The values' ranks among the candidates, and across CTAs by binary
+// that between k and 512 reach.  12288 rows x 50257 bf16: 192 us without a list (6.4 TB/s), 214 with one
+// entry, 226 with 20, 253 with 64.  The values' ranks among the candidates, and across CTAs by binary
 // search in the others' lists, are their places in the list.
 template <typename E, int NT>
-__global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
+__global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
     griddep_launch_dependents();
     __shared__ float red[NT / 32], red_s[NT / 32], red_t[NT / 32];
     __shared__ int ired[NT / 32];
@@ -366,18 +366,17 @@ __global__ void __launch_bounds__(NT, 1024 / NT) logprobs_kernel(const E* __rest
             if (lane == 31 && upto > 0) base = atomicAdd(counter, upto);
             return __shfl_sync(0xffffffffu, base, 31) + upto - n;
         };
-        {   // this thread's steps that reach the bound (at most 64 slots), and its element outside the units
-            unsigned long long in = 0;
-            uint32_t end = 0;
+        {   // this thread's steps that reach the bound (at most 32 slots), and its element outside the units
+            uint32_t in = 0, end = 0;
             if (my_key >= bound16) {
                 const uint32_t n = (step + (1u << a.slot_shift) - 1) >> a.slot_shift;
 #pragma unroll 8
-                for (uint32_t j = 0; j < n; ++j) in |= static_cast<unsigned long long>(!(slot_value(slots[j][tid]) < bound)) << j;
+                for (uint32_t j = 0; j < n; ++j) in |= static_cast<uint32_t>(!(slot_value(slots[j][tid]) < bound)) << j;
                 end = first < row.ends && !(z_end < bound);
             }
-            uint32_t at = reserve(__popcll(in), &s_hits);
+            uint32_t at = reserve(__popc(in), &s_hits);
             for (; in; in &= in - 1, ++at)
-                if (at < kHits) hits[at] = static_cast<uint32_t>(__ffsll(in) - 1) << 16 | tid;
+                if (at < kHits) hits[at] = static_cast<uint32_t>(__ffs(in) - 1) << 16 | tid;
             if (warp == 0) {   // (the elements outside the units are the first threads')
                 at = reserve(end, &s_count);
                 if (end && at < kCandidates) cand[at] = entry(z_end, row.end_col(first));
@@ -574,7 +573,7 @@ GPT_DEVINL uint4 grad_unit(const RowGrad& q, const uint4& w, uint32_t hit, const
     for (int i = 0; i < 4; ++i) {
         float a, b;
         f2_unpack(q.two(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), a, b);
-        if (hit < 8) {   // the token's column is one of these eight
+        if (hit < 8) {   // the token's column is one of these nine (bf16) or eight (fp32)
             if (hit == 2 * i) a += q.g;
             if (hit == 2 * i + 1) b += q.g;
         }
@@ -658,6 +657,7 @@ template <typename E>
 int launch_score(const E* logits, const ScoreArgs& a, int rows, cudaStream_t s) {
     if (a.cluster > 1)
         return launch_overlapped_cluster(logprobs_kernel<E, 256>, a.cluster, dim3(rows * a.cluster), dim3(256), 0, s, logits, a);
+    if (a.threads == 256) return launch_overlapped(logprobs_kernel<E, 256>, dim3(rows), dim3(256), 0, s, logits, a);
     return launch_overlapped(logprobs_kernel<E, 128>, dim3(rows), dim3(128), 0, s, logits, a);
 }
 
@@ -691,7 +691,9 @@ int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int
     int cluster = kMaxCluster;
     while (cluster > 1 && (static_cast<long long>(rows) * cluster > 148 || V < cluster * 2048)) cluster /= 2;
     a.cluster = cluster;
-    const long long step = static_cast<long long>(cluster > 1 ? 256 : 128) * cluster * kUnroll * (dtype == GPT_DTYPE_BF16 ? 8 : 4);
+    // few rows: twice the loads in flight per row (519 rows x 50257 fp32, 20 entries: 24.6 against 29.3 us)
+    a.threads = cluster > 1 || (rows <= 148 * 4 && V >= 8192) ? 256 : 128;
+    const long long step = static_cast<long long>(a.threads) * cluster * kUnroll * (dtype == GPT_DTYPE_BF16 ? 8 : 4);
     while ((V + step - 1) / step > static_cast<long long>(kSlots) << a.slot_shift) ++a.slot_shift;
     return dtype == GPT_DTYPE_BF16 ? launch_score(static_cast<const bf16*>(logits), a, rows, s)
                                    : launch_score(static_cast<const float*>(logits), a, rows, s);
