@@ -98,7 +98,8 @@ class GPT:
         """One greedy step over drafted trees: runs the nodes tok int64 [B, N] (parents int32 [B, N], -1 for a
         root, -2 for no node) over the cache's first lengths int32 [B] positions, takes the likeliest token at
         each node, and keeps the path that the choices confirm (its k, v go into the cache).  Returns
-        (native.TreeAccept, chosen int64 [B, N]); the kept tokens are chosen along the path."""
+        (native.TreeAccept, chosen int64 [B, N]); the kept tokens are chosen along the path.  Calls of a model
+        share its workspace and node buffers: order them on one stream."""
         B, N = tok.shape
         key = ("tree", B, N)
         if key not in self._host:

@@ -878,7 +878,8 @@ GPT_API int gpt_tree_attention(const void* qkv, const void* kv, const int32_t* l
     if (!tree_size_ok(B, N, nh)) return GPT_ERR_UNSUPPORTED;
     if (dtype == GPT_DTYPE_BF16 ? hs != 64 : (hs % 8 || hs > 128)) return GPT_ERR_UNSUPPORTED;
     if (nh > 0x7fffffff / 4 / hs || block_size > 0x7fffffff - 1024) return GPT_ERR_UNSUPPORTED;
-    if (!aligned(qkv, 16) || !aligned(kv, 16) || !aligned(y, 16) || !aligned(lengths, 4) || !aligned(parents, 4))
+    if (!aligned(qkv, 16) || !aligned(kv, 16) || !aligned(y, 16) || !aligned(lengths, 4) || !aligned(parents, 4) ||
+        !aligned(status, 4))
         return GPT_ERR_BAD_ALIGN;
     return launch_tree_attention(dtype, qkv, kv, lengths, parents, y, B, N, nh, hs, block_size, status,
                                  static_cast<cudaStream_t>(stream));
@@ -898,7 +899,9 @@ GPT_API int gpt_tree_step(const gpt_config_t* cfg, const void* weights, const in
     if (!tok || !parents || !lengths || !kv_cache || !tree_qkv || !logits) return GPT_ERR_NULL;
     if (!tree_size_ok(B, N, cfg->n_head)) return GPT_ERR_UNSUPPORTED;
     if (cfg->dtype == GPT_DTYPE_BF16 && cfg->vocab_size % 8) return GPT_ERR_UNSUPPORTED;
-    if (!aligned(kv_cache, 16) || !aligned(tree_qkv, 16) || !aligned(logits, 16)) return GPT_ERR_BAD_ALIGN;
+    if (!aligned(kv_cache, 16) || !aligned(tree_qkv, 16) || !aligned(logits, 16) || !aligned(tok, 8) ||
+        !aligned(parents, 4) || !aligned(lengths, 4))
+        return GPT_ERR_BAD_ALIGN;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     Weights W;
     fill_weights(W, cfg, weights);
@@ -940,7 +943,10 @@ GPT_API int gpt_tree_accept(const gpt_config_t* cfg, const int32_t* parents, con
     if (!tree_size_ok(B, N, cfg->n_head)) return GPT_ERR_UNSUPPORTED;
     const long long c_bytes = static_cast<long long>(cfg->n_embd) * elem_size(cfg);
     if (cfg->n_layer > 0x7fffffffLL / GPT_TREE_MAX_NODES / (2 * c_bytes / 16)) return GPT_ERR_UNSUPPORTED;
-    if (!aligned(tree_qkv, 16) || !aligned(kv_cache, 16)) return GPT_ERR_BAD_ALIGN;
+    if (!aligned(tree_qkv, 16) || !aligned(kv_cache, 16) || !aligned(tok, 8) || !aligned(chosen, 8) ||
+        !aligned(next_token, 8) || !aligned(parents, 4) || !aligned(lengths, 4) || !aligned(path, 4) ||
+        !aligned(n_accepted, 4) || !aligned(lengths_out, 4) || !aligned(status, 4))
+        return GPT_ERR_BAD_ALIGN;
     return launch_tree_accept(parents, tok, chosen, lengths, B, N, cfg->n_layer, tree_qkv, kv_cache, c_bytes,
                               cfg->block_size, path, n_accepted, next_token, lengths_out, status,
                               static_cast<cudaStream_t>(stream));
@@ -965,6 +971,9 @@ GPT_API int gpt_token_logprobs(const void* logits, long long ld, const int64_t* 
     if (k < 0 || k > V) return GPT_ERR_BAD_SHAPE;
     if ((logp && !tokens) || (k > 0 && (!top_ids || !top_logp))) return GPT_ERR_NULL;
     if (k > GPT_TOP_MAX) return GPT_ERR_UNSUPPORTED;
+    if (!aligned(tokens, 8) || !aligned(logp, 4) || !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_ids, 8) ||
+        !aligned(top_logp, 4) || !aligned(status, 4))
+        return GPT_ERR_BAD_ALIGN;
     if (rows == 0) return GPT_OK;
     return launch_logprobs(logits, ld, tokens, rows, V, dtype, temperature, logp, entropy, lse, k, top_ids, top_logp,
                            status, static_cast<cudaStream_t>(stream));
@@ -977,7 +986,9 @@ GPT_API int gpt_token_logprobs_backward(const void* logits, long long ld, const 
     GPT_TRY(check_logprobs(logits, ld, rows, V, dtype, temperature));
     if (!lse || !dlogits || (dlogp && !tokens) || (dentropy && !entropy)) return GPT_ERR_NULL;
     if (ldd < V || (logits == dlogits && ld != ldd)) return GPT_ERR_BAD_SHAPE;
-    if (!aligned(dlogits, dtype == GPT_DTYPE_BF16 ? 2 : 4)) return GPT_ERR_BAD_ALIGN;
+    if (!aligned(dlogits, dtype == GPT_DTYPE_BF16 ? 2 : 4) || !aligned(tokens, 8) || !aligned(lse, 4) ||
+        !aligned(entropy, 4) || !aligned(dlogp, 4) || !aligned(dentropy, 4) || !aligned(status, 4))
+        return GPT_ERR_BAD_ALIGN;
     if (rows == 0) return GPT_OK;
     return launch_logprobs_backward(logits, ld, tokens, rows, V, dtype, temperature, lse, entropy, dlogp, dentropy,
                                     dlogits, ldd, status, static_cast<cudaStream_t>(stream));

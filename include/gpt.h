@@ -332,7 +332,7 @@ int gpt_generate(const gpt_config_t* cfg, const void* weights, const int64_t* id
  * (A(i)); it sits at position lengths[b] + |A(i)| - 1.  lengths int32 [B] lie in [0, block_size]; one
  * outside records GPT_ERR_BAD_SHAPE and is clamped.
  * Buffers of one layer: the cache [B, block_size, 2, C] (gpt_kv_cache_bytes' layout) and the nodes'
- * q, k, v [B, N, 3, C], the c_attn output. */
+ * q, k, v [B, N, 3, C], the c_attn output.  Integer arrays are aligned to their element. */
 #define GPT_TREE_MAX_NODES 64
 
 /* Attention of the nodes over the cache and their ancestors:

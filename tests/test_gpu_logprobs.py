@@ -227,6 +227,23 @@ def test_streams_and_graph_replay():
         xin.zero_()
 
 
+def test_calls_at_once():
+    """Calls in flight together on two streams share nothing."""
+    from decoder_only_transformer_causal_b200 import native
+    xs = [make(rows, V, dt) for rows, V, dt in ((700, 9001, "bf16"), (9, 50257, "f32"))]
+    xs = [(z.cuda(), t.cuda()) for z, t in xs]
+    want = [native.token_logprobs(z, t, k=7) for z, t in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(native.token_logprobs(*xs[i], k=7))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i in range(2) for r in got[i] for a, b in zip(r, want[i]))
+
+
 # ------------------------------------------------------------------ gradient
 def check_grad(z, tok, g, h, T, x=None, out=None):
     from decoder_only_transformer_causal_b200 import native

@@ -90,6 +90,8 @@ CASES = [
     (4, 33, 2, 300, [0, 128, 300, 5]), (4, 48, 3, 400, [400, 129, 65, 1]), (4, 64, 2, 700, [700, 640, 64, 0]),
     (1, 64, 1, 5000, [4999]), (1, 5, 1, 9000, [8191]), (70, 3, 16, 130, [(13 * i) % 131 for i in range(70)]),
     (12, 64, 16, 70, [6 * i for i in range(12)]),
+    (40, 50, 12, 300, [(77 * i) % 301 for i in range(40)]),      # more pairs than run at a time, 64-row groups
+    (200, 2, 2, 40, [(7 * i) % 41 for i in range(200)]),         # ... and too many sequences to order
 ]
 
 
@@ -204,6 +206,26 @@ def test_tree_attention_streams_and_graph_replay(N, dtype):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_tree_attention_calls_at_once(dtype):
+    """Calls in flight together on two streams share nothing."""
+    from decoder_only_transformer_causal_b200 import native
+    args, want = [], []
+    for N, nh in ((5, 12), (40, 12)):
+        y, _, d = run_attention(30, N, nh, 64, 400, [(37 * i) % 401 for i in range(30)], random_parents(30, N, N), dtype, seed=N)
+        args.append(d + [nh])
+        want.append(y)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(native.tree_attention(*args[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
 
 
 # ------------------------------------------------------------------ the model over a tree

@@ -76,6 +76,19 @@ def test_tree_accept_refusals():
     assert L.gpt_tree_accept(None, *([FAKE] * 4), 1, 1, *([FAKE] * 6), None, None) == NULL
 
 
+def test_index_arrays_must_be_aligned():
+    c = _cfg()
+    for name in ("tok", "par", "lens"):
+        assert step(c, **{name: FAKE + 2}) == ALIGN, name
+    for name in ("par", "tok", "cho", "lens", "path", "n", "nxt", "lo"):
+        assert accept(c, **{name: FAKE + 2}) == ALIGN, name
+    assert accept(c, tok=FAKE + 4) == ALIGN and accept(c, nxt=FAKE + 4) == ALIGN
+    assert score(tok=FAKE + 4) == ALIGN and score(logp=FAKE + 2) == ALIGN
+    assert score(k=1, ids=FAKE + 4, lp=FAKE) == ALIGN and score(k=1, ids=FAKE, lp=FAKE + 1) == ALIGN
+    for name in ("lse", "ent", "g", "h"):
+        assert grad(**{name: FAKE + 2}) == ALIGN, name
+
+
 def test_tree_qkv_bytes():
     c = _cfg()
     assert L.gpt_tree_qkv_bytes(ctypes.byref(c.c()), 3, 5) == 12 * 3 * 5 * 3 * 768 * 2
