@@ -684,7 +684,7 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
     __shared__ unsigned long long see[kMaxNodes], s_bad;
     __shared__ uint64_t full[STAGES], empty[STAGES];
     __shared__ int par[kMaxNodes];
-    __shared__ float2 ml[ROWS];
+    __shared__ float2 ml[2][ROWS], joined_ml[ROWS];
     __shared__ int s_abort;
     volatile int* abort_flag = &s_abort;
     const int hs = a.hs, N = a.N;
@@ -727,14 +727,16 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
     // The queries as operand fragments.  Step 2c + e of a chunk of 16 dimensions takes dimensions
     // 16 c + 4 t + 2 e (k = t) and the next one (k = t + 4), so that a thread's K values are 16 bytes.
     const int n_steps = 2 * ((hs + 15) / 16);
+#pragma unroll 4
     for (int it = tid; it < n_steps * MT * NG * 32; it += block_threads(NG)) {
         const int l = it & 31, tile = (it >> 5) % (MT * NG), s = (it >> 5) / (MT * NG);
         const int row = tile * 16 + (l >> 2), dim = (s >> 1) * 16 + (l & 3) * 4 + (s & 1) * 2;
         uint32_t hi[4], lo[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = row + (e & 1) * 8, d = dim + (e >> 1);
-            split(i < N && d < hs ? __ldcg(node + i * 3 * C + d) : 0.f, hi[e], lo[e]);
+        for (int e = 0; e < 2; ++e) {
+            const int i = row + e * 8;
+            const float2 q = i < N && dim < hs ? __ldcg(reinterpret_cast<const float2*>(node + i * 3 * C + dim)) : make_float2(0.f, 0.f);
+            split(q.x, hi[e], lo[e]), split(q.y, hi[e + 2], lo[e + 2]);
         }
         sQ[((s * MT * NG + tile) * 2) * 32 + l] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         sQ[((s * MT * NG + tile) * 2 + 1) * 32 + l] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
@@ -919,7 +921,8 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
     }
     __syncthreads();
 
-    // The warps' parts joined one after another in the ring's place, then the CTAs'.
+    // In the ring's place: the first and third key warp leave their parts, the second and fourth join theirs to
+    // them, then the two, then the CTAs'.
     float* sO = reinterpret_cast<float*>(ring);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
@@ -928,14 +931,15 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
             l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 1);
             l[mt][r] += __shfl_xor_sync(0xffffffffu, l[mt][r], 2);
         }
-    for (int w = 0; w < 4; ++w) {
-        if (key_warp == w && tid < THREADS) {
+    const int half = key_warp >> 1;
+    for (int w = 0; w < 2; ++w) {
+        if ((key_warp & 1) == w && tid < THREADS) {
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
                     const int i = (group * MT + mt) * 16 + g + 8 * r;
-                    const float2 old = w ? ml[i] : make_float2(-INFINITY, 0.f);
+                    const float2 old = w ? ml[half][i] : make_float2(-INFINITY, 0.f);
                     const bool have_old = old.y != 0.f, have = l[mt][r] != 0.f;
                     const float M = have_old ? have ? fmaxf(old.x, m[mt][r]) : old.x : m[mt][r];
                     const float f_old = !have_old ? 0.f : old.x == M ? 1.f : exp2_approx(old.x - M);
@@ -944,7 +948,7 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
                     for (int p = 0; p < P; ++p)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {   // four dimensions
-                            float4* at = reinterpret_cast<float4*>(sO + i * LD + p * 32 + 8 * t4 + 4 * e);
+                            float4* at = reinterpret_cast<float4*>(sO + (half * ROWS + i) * LD + p * 32 + 8 * t4 + 4 * e);
                             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
                             if (have_old) v = *at;
                             if (have_old) v.x *= f_old, v.y *= f_old, v.z *= f_old, v.w *= f_old;
@@ -955,17 +959,44 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
                             *at = v;
                         }
                     __syncwarp();
-                    if (t4 == 0) ml[i] = make_float2(M, (have_old ? old.y * f_old : 0.f) + (have ? l[mt][r] * f : 0.f));
+                    if (t4 == 0) ml[half][i] = make_float2(M, (have_old ? old.y * f_old : 0.f) + (have ? l[mt][r] * f : 0.f));
                 }
         }
         __syncthreads();
     }
+    const bool alone = a.cluster == 1;
+    float* out = y + static_cast<long long>(b) * N * C + h * hs;
+    unsigned long long bad = s_bad;
+    for (int it = tid; it < N * 4 * P; it += block_threads(NG)) {
+        const int i = it / (4 * P), d = it % (4 * P) * 8;
+        if (d >= hs) continue;
+        Joined x;
+        const float2 m0 = ml[0][i], m1 = ml[1][i];
+        x.see(m0), x.see(m1);
+        float* o0 = sO + i * LD + d;
+        const float* o1 = o0 + ROWS * LD;
+        if (m0.y != 0.f) x.add(m0, reinterpret_cast<const float4*>(o0)[0], reinterpret_cast<const float4*>(o0)[1]);
+        if (m1.y != 0.f) x.add(m1, reinterpret_cast<const float4*>(o1)[0], reinterpret_cast<const float4*>(o1)[1]);
+        if (alone) {
+            if (see[i]) {
+                x.finish(bad & see[i], node + 2 * C + d, 3 * C);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x.o[e] = 0.f;
+            }
+            st8(out + i * C + d, x.o);
+        } else {
+            st8(o0, x.o);
+            if (d == 0) joined_ml[i] = make_float2(x.M, x.L);
+        }
+    }
+    if (alone) return;
+    __syncwarp();
     cluster_sync();
     const int holder = n_cache % a.cluster;   // of the nodes' tile
-    const unsigned long long bad =
-        static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&s_bad) + 1, holder))) << 32 |
-        ld_cluster_u32(map_to_rank(&s_bad, holder));
-    join_cluster(sO, LD, ml, see, a, hs / 8, rank, y + static_cast<long long>(b) * N * C + h * hs, C,
+    bad = static_cast<unsigned long long>(ld_cluster_u32(map_to_rank(reinterpret_cast<uint32_t*>(&s_bad) + 1, holder))) << 32 |
+          ld_cluster_u32(map_to_rank(&s_bad, holder));
+    join_cluster(sO, LD, joined_ml, see, a, hs / 8, rank, out, C,
                  [&](int i, int d, Joined& x) { x.finish(bad & see[i], node + 2 * C + d, 3 * C); });
     __syncwarp();
     cluster_sync();
