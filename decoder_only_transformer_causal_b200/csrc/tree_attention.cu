@@ -1039,10 +1039,14 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
     const long long pairs = static_cast<long long>(B) * nh;
     const int tiles = (block_size - 1) / (is_f32 ? f32::KEYS : tc::KEYS) + 2;
     a.cluster = 1;
-    // CTAs that run at a time
+    // As many CTAs as run at a time; twice as many where a CTA keeps at least 24 tiles (fp32, whose tiles take
+    // longer: 8), so that long sequences do not outlast the rest.  bf16, 12 x 20 nodes x 16 heads up to 8192
+    // keys: 52 us with 2 CTAs a pair, 72 with 1; 18 x 20 x 16 up to 4096 keys: 43 and 43; 8 x 20 x 25 up to 1024:
+    // 21 and 15.  fp32, 3 x 50 x 16 up to 2000 keys: 71, 52 and 86 us with 2, 4 and 8.
     const long long slots = 148 * (!is_f32 ? 2 : hs > 64 || N > 32 ? 1 : N > 16 ? 2 : 3);
+    const int keep = is_f32 ? 8 : 24;
     while (a.cluster < 8 && a.cluster < tiles &&
-           (pairs * a.cluster * 2 <= slots || (pairs * a.cluster * 2 <= 2 * slots && tiles >= 48 * a.cluster)))
+           (pairs * a.cluster * 2 <= slots || (pairs * a.cluster <= slots && tiles >= keep * 2 * a.cluster)))
         a.cluster *= 2;
     // more CTAs than run at a time: those with the most work start first
     a.longest_first = !is_f32 && B > 1 && B <= tc::THREADS && pairs * a.cluster > slots;
