@@ -647,8 +647,24 @@ __global__ void __launch_bounds__(kThreads)
                 const uint32_t col = z.end_col(first);
                 st(d + col, q.one(ld_act(z.z + col), col == tok));
             }
-        } else {   // rows that start at different places of a 16-byte unit
-            for (uint32_t col = first; col < a.V; col += z.stride) st(d + col, q.one(ld_act(z.z + col), col == tok));
+        } else {   // rows that start at different places of a 16-byte unit: by element, eight loads in flight
+            // (6035 rows x 27626 bf16: 147 us, 375 with one load in flight)
+            constexpr int kEach = 8;
+            uint32_t col = first;
+            for (; a.V > (kEach - 1) * z.stride && col < a.V - (kEach - 1) * z.stride; col += kEach * z.stride) {
+                float v[kEach];
+#pragma unroll
+                for (int i = 0; i < kEach; ++i) v[i] = ld_act(z.z + col + i * z.stride);
+#pragma unroll
+                for (int i = 0; i < kEach; i += 2) {
+                    float x, y;
+                    f2_unpack(q.two(v[i], v[i + 1]), x, y);
+                    const uint32_t c0 = col + i * z.stride, c1 = c0 + z.stride;
+                    st(d + c0, c0 == tok ? x + q.g : x);
+                    st(d + c1, c1 == tok ? y + q.g : y);
+                }
+            }
+            for (; col < a.V; col += z.stride) st(d + col, q.one(ld_act(z.z + col), col == tok));
         }
     }
 }
