@@ -354,18 +354,6 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
     if (a.k > 0) {
         const uint32_t bound16 = s_bound;
         const float bound = bound16 == 0 ? -INFINITY : bound16 == 0xffffu ? INFINITY : key_value(bound16 << 16);
-        // places for n entries of each lane, one addition to the counter per warp
-        auto reserve = [&](uint32_t n, uint32_t* counter) {
-            uint32_t upto = n;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
-                if (lane >= o) upto += v;
-            }
-            uint32_t base = 0;
-            if (lane == 31 && upto > 0) base = atomicAdd(counter, upto);
-            return __shfl_sync(0xffffffffu, base, 31) + upto - n;
-        };
         {   // this thread's steps that reach the bound (at most 32 slots), and its element outside the units
             uint32_t in = 0, end = 0;
             if (my_key >= bound16) {
@@ -374,12 +362,12 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
                 for (uint32_t j = 0; j < n; ++j) in |= static_cast<uint32_t>(!(slot_value(slots[j][tid]) < bound)) << j;
                 end = first < row.ends && !(z_end < bound);
             }
-            uint32_t at = reserve(__popc(in), &s_hits);
+            uint32_t at = in ? atomicAdd(&s_hits, static_cast<uint32_t>(__popc(in))) : 0;
             for (; in; in &= in - 1, ++at)
                 if (at < kHits) hits[at] = static_cast<uint32_t>(__ffs(in) - 1) << 16 | tid;
-            if (warp == 0) {   // (the elements outside the units are the first threads')
-                at = reserve(end, &s_count);
-                if (end && at < kCandidates) cand[at] = entry(z_end, row.end_col(first));
+            if (end) {
+                at = atomicAdd(&s_count, 1u);
+                if (at < kCandidates) cand[at] = entry(z_end, row.end_col(first));
             }
         }
         __syncthreads();
@@ -410,7 +398,8 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
                     }
                     n += __popc(in[x]);
                 }
-                uint32_t at = reserve(n, &s_count);
+                if (n == 0) continue;
+                uint32_t at = atomicAdd(&s_count, n);
 #pragma unroll
                 for (int x = 0; x < 4; ++x)
                     for (; in[x]; in[x] &= in[x] - 1, ++at) {
