@@ -14,8 +14,8 @@ constexpr int kThreads = 256;
 constexpr int kUnrollLog2 = 2;
 constexpr int kUnroll = 1 << kUnrollLog2;   // 16-byte loads in flight per thread
 constexpr int kMaxCluster = 4;
-constexpr int kCandidates = 512;    // places for the values at or above a part's top-k bound
-constexpr int kHits = 512;          // places for the steps that reach the bound
+// Places for the values at or above a part's top-k bound, and for the steps that reach it.
+constexpr uint32_t places(int threads) { return threads < 64 ? 256 : 512; }   // (candidates fit where the slots were)
 constexpr int kSlots = 32;          // places per thread for the maxima of its steps (of kUnroll loads)
 
 template <typename E> constexpr int kVec = 16 / sizeof(E);
@@ -195,10 +195,11 @@ struct ScoreArgs {
     int32_t* status;
 };
 
-// A row is read once from HBM by a cluster of 1, 2 or 4 CTAs, 16 bytes per load.  Many rows: 128 threads
-// each, nine (bf16) or eight (fp32) rows per SM: with 256 threads the ends of the rows (reductions, the list)
-// left the memory idle (228 us against 206 without a list); two steps in flight per thread cost a quarter of the threads and were slower
-// (313 against 265 us with 20 entries), as was asking L2 for the next row (325 against 228).
+// A row is read once from HBM by a cluster of 1, 2 or 4 CTAs, 16 bytes per load.  Many rows: 32, 64 or 128
+// threads each (the launch has the rule), the SM's registers full of rows: with 256 threads the ends of the rows
+// (reductions, the list) left the memory idle (228 us against 206 without a list); two steps in flight per thread
+// cost a quarter of the threads and were slower (313 against 265 us with 20 entries), as was asking L2 for the
+// next row (325 against 228).
 //
 // Sums.  Each thread keeps a running maximum, raised once per 64 bytes, and the sums relative to it; the
 // threads' and then the CTAs' sums are joined in a fixed order.  Values are first raised to floor_z, so
@@ -208,23 +209,29 @@ struct ScoreArgs {
 //
 // Top list.  The k-th largest of the CTA's thread maxima is a bound that at least k of its values
 // reach, and hardly more do: only the steps whose maximum reaches it (about k of them) are read
-// again, from L2.  More than 512 such values (long ties): a bisection over (value, index) finds a bound
-// that between k and 512 reach.  12288 rows x 50257 bf16: 192 us without a list (6.4 TB/s), 214 with one
-// entry, 226 with 20, 253 with 64.  The values' ranks among the candidates, and across CTAs by binary
-// search in the others' lists, are their places in the list.
+// again, from L2.  More such values than places (long ties): a bisection over (value, index) finds a bound
+// that no more than fit reach.  12288 rows x 50257 bf16: 192 us without a list (6.4 TB/s), 206 with one
+// entry, 226 with 20, 260 with 64.  The values' ranks among the candidates, and across CTAs by binary search in
+// the others' lists, are their places in the list.
 template <typename E, int NT>
-__global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
+__global__ void __launch_bounds__(NT, NT > 128 ? 4 : NT == 32 ? 32 : (sizeof(E) == 2 ? 9 : 8) * 128 / NT)
+logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
+    constexpr uint32_t kPlaces = places(NT);
     griddep_launch_dependents();
     __shared__ float red[NT / 32], red_s[NT / 32], red_t[NT / 32];
     __shared__ int ired[NT / 32];
-    __shared__ __align__(16) unsigned long long cand[kCandidates];
-    __shared__ unsigned long long lists[NT == 128 ? 1 : kMaxCluster][GPT_TOP_MAX];
+    // the candidates lie where the slots were: shared memory is taken from the L1 that the loads in flight need
+    // (9000 rows x 9001 bf16, 20 entries: 57.0 us with 10.9 KB per row of 64 threads, 52.5 with 6.8)
+    __shared__ __align__(16) uint16_t slots[kSlots][NT];
+    static_assert(sizeof(slots) >= kPlaces * sizeof(unsigned long long));
+    unsigned long long* cand = reinterpret_cast<unsigned long long*>(slots);
+    __shared__ unsigned long long lists[NT < 256 ? 1 : kMaxCluster][GPT_TOP_MAX];
     __shared__ Part parts[kMaxCluster];
-    __shared__ uint16_t slots[kSlots][NT], keys[NT];
-    __shared__ uint32_t hits[kHits];
+    __shared__ uint16_t keys[NT];
+    __shared__ uint32_t hits[kPlaces];
     __shared__ uint32_t s_bound, s_hits, s_count;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int ncta = NT == 128 ? 1 : a.cluster;   // (known to the compiler for CTAs that are alone)
+    const int ncta = NT < 256 ? 1 : a.cluster;   // (known to the compiler for CTAs that are alone)
     const int rank = ncta > 1 ? static_cast<int>(cluster_ctarank()) : 0;
     if (ncta > 1) asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
     const long long r = blockIdx.x / ncta;
@@ -354,8 +361,9 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
     if (a.k > 0) {
         const uint32_t bound16 = s_bound;
         const float bound = bound16 == 0 ? -INFINITY : bound16 == 0xffffu ? INFINITY : key_value(bound16 << 16);
-        {   // this thread's steps that reach the bound (at most 32 slots), and its element outside the units
-            uint32_t in = 0, end = 0;
+        uint32_t end = 0;   // this thread's element outside the units reaches the bound
+        {   // this thread's steps that do (at most 32 slots)
+            uint32_t in = 0;
             if (my_key >= bound16) {
                 const uint32_t n = (step + (1u << a.slot_shift) - 1) >> a.slot_shift;
 #pragma unroll 8
@@ -364,15 +372,15 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
             }
             uint32_t at = in ? atomicAdd(&s_hits, static_cast<uint32_t>(__popc(in))) : 0;
             for (; in; in &= in - 1, ++at)
-                if (at < kHits) hits[at] = static_cast<uint32_t>(__ffs(in) - 1) << 16 | tid;
-            if (end) {
-                at = atomicAdd(&s_count, 1u);
-                if (at < kCandidates) cand[at] = entry(z_end, row.end_col(first));
-            }
+                if (at < kPlaces) hits[at] = static_cast<uint32_t>(__ffs(in) - 1) << 16 | tid;
         }
-        __syncthreads();
+        __syncthreads();   // (the slots are done with)
+        if (end) {
+            const uint32_t at = atomicAdd(&s_count, 1u);
+            if (at < kPlaces) cand[at] = entry(z_end, row.end_col(first));
+        }
         const uint32_t n_hits = s_hits, each_log2 = kUnrollLog2 + a.slot_shift;
-        if (n_hits <= kHits)
+        if (n_hits <= kPlaces)
             for (uint32_t i0 = warp * 32; i0 < n_hits << each_log2; i0 += 4 * NT) {   // four units per lane at a time
                 uint4 w[4];
                 uint32_t cols[4], in[4], n = 0;
@@ -406,12 +414,12 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
                         const uint32_t e = __ffs(in[x]) - 1, pos = sizeof(E) == 4 ? e : e >> 1;
                         const uint32_t bits = pos == 0 ? w[x].x : pos == 1 ? w[x].y : pos == 2 ? w[x].z : w[x].w;
                         const float z = __uint_as_float(sizeof(E) == 4 ? bits : (e & 1) ? bits & 0xffff0000u : bits << 16);
-                        if (at < kCandidates) cand[at] = entry(z, cols[x] + e);
+                        if (at < kPlaces) cand[at] = entry(z, cols[x] + e);
                     }
             }
         __syncthreads();
         uint32_t count = s_count;
-        if (count > kCandidates || n_hits > kHits) {
+        if (count > kPlaces || n_hits > kPlaces) {
             // the largest bound over (value, index) that at least k entries reach, bit by bit until few do
             unsigned long long at_least = 0;
             for (int bit = 63; bit >= 0; --bit) {
@@ -421,7 +429,7 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
                 above = block_reduce<NT>(above, ired, [](int x, int y) { return x + y; });
                 if (above >= a.k) {
                     at_least = at;
-                    if (above <= kCandidates) break;
+                    if (above <= kPlaces) break;
                 }
             }
             __syncthreads();
@@ -435,8 +443,8 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
             count = s_count;
         }
         // places by counting
-        const uint32_t padded = (count + 7) & ~7u;   // (at most kCandidates)
-        if (tid < padded - count) cand[count + tid] = 0;
+        const uint32_t padded = (count + 7) & ~7u;   // (at most kPlaces)
+        if (tid < static_cast<int>(padded - count)) cand[count + tid] = 0;
         __syncthreads();
         for (uint32_t i = tid; i < count; i += NT) {
             const unsigned long long e = cand[i];
@@ -450,7 +458,8 @@ __global__ void __launch_bounds__(NT, NT > 128 ? 4 : sizeof(E) == 2 ? 9 : 8) log
             }
             if (place < a.k) list[place] = e;
         }
-        if (tid >= static_cast<int>(count) && tid < a.k) list[tid] = 0;   // a part shorter than k
+        for (int i = tid; i < a.k; i += NT)
+            if (i >= static_cast<int>(count)) list[i] = 0;   // a part shorter than k
         __syncthreads();
     }
     if (ncta > 1) {
@@ -663,6 +672,8 @@ int launch_score(const E* logits, const ScoreArgs& a, int rows, cudaStream_t s) 
     if (a.cluster > 1)
         return launch_overlapped_cluster(logprobs_kernel<E, 256>, a.cluster, dim3(rows * a.cluster), dim3(256), 0, s, logits, a);
     if (a.threads == 256) return launch_overlapped(logprobs_kernel<E, 256>, dim3(rows), dim3(256), 0, s, logits, a);
+    if (a.threads == 32) return launch_overlapped(logprobs_kernel<E, 32>, dim3(rows), dim3(32), 0, s, logits, a);
+    if (a.threads == 64) return launch_overlapped(logprobs_kernel<E, 64>, dim3(rows), dim3(64), 0, s, logits, a);
     return launch_overlapped(logprobs_kernel<E, 128>, dim3(rows), dim3(128), 0, s, logits, a);
 }
 
@@ -696,8 +707,21 @@ int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int
     int cluster = kMaxCluster;
     while (cluster > 1 && (static_cast<long long>(rows) * cluster > 148 || V < cluster * 2048)) cluster /= 2;
     a.cluster = cluster;
-    // few rows: twice the loads in flight per row (519 rows x 50257 fp32, 20 entries: 24.6 against 29.3 us)
-    a.threads = cluster > 1 || (rows <= 148 * 4 && V >= 8192) ? 256 : 128;
+    // Threads per row, from the 16-byte units of a row (measured at every power of two; us with 0 / 1 / 20
+    // alternatives).  More than a wave of 128-thread CTAs: a row's end (reductions, the list) costs a CTA about
+    // the same however many threads it has, so that short rows want few.  9000 rows x 2057 bf16: 32 threads
+    // 12.4 / 17.6 / 23.2, 64: 13.4 / 27.3 / 32.1, 128: 19.1 / 36.0 / 40.7; 9000 x 5000 bf16: 25.5 / 31.7 / 37.8,
+    // 23.2 / 36.6 / 41.7, 30.2 / 48.1 / 52.5; 9000 x 9001 fp32: 66.3 / 72.9 / 92.7, 56.7 / 68.7 / 73.9, 60.0 / 80.9 /
+    // 84.9.  Long rows want enough CTAs for several waves as well: 2000 x 32000 bf16: 64 threads 30.1 / 34.2 / 35.7,
+    // 128: 27.9 / 33.0 / 34.6; 12288 x 50257: 191.8 / 205.7 / 226, 193.7 / 214.1 / 227, 40 entries 253 and 242.  The list's bound needs more threads than entries: 64 threads with 64 entries fall
+    // back to the bisection (8805 x 2057: 195 against 58 us).
+    // At most four rows per SM: twice the loads in flight once a row or all of them are long (592 x 50257 bf16:
+    // 256 threads 15.0 / 18.0 / 18.5, 128: 17.6 / 20.3 / 20.8; 300 rows: 11.4 / 14.2 / 14.7, 9.8 / 12.4 / 12.9).
+    const long long row_units = (static_cast<long long>(V) * (dtype == GPT_DTYPE_BF16 ? 2 : 4) + 15) / 16;
+    a.threads = 128;
+    if (cluster > 1 || (rows <= 148 && row_units >= 2048) || (rows <= 148 * 4 && rows * row_units >= 1 << 21)) a.threads = 256;
+    else if (rows > 148 * 9 && k <= 20 && row_units <= (k ? 640 : 512)) a.threads = 32;
+    else if (rows > 148 * 9 && k <= 40 && (row_units <= 1280 || (k <= 20 && 2ll * rows >= 3 * row_units))) a.threads = 64;
     const long long step = static_cast<long long>(a.threads) * cluster * kUnroll * (dtype == GPT_DTYPE_BF16 ? 8 : 4);
     while ((V + step - 1) / step > static_cast<long long>(kSlots) << a.slot_shift) ++a.slot_shift;
     return dtype == GPT_DTYPE_BF16 ? launch_score(static_cast<const bf16*>(logits), a, rows, s)

@@ -31,11 +31,13 @@ def close(got, ref, tol, what):
     assert np.array_equal(np.isnan(got), np.isnan(ref)), what
     assert np.array_equal(got[np.isinf(ref)], ref[np.isinf(ref)]), what
     with np.errstate(invalid="ignore"):
+        # a row without a finite maximum has no bound (NaN): what is finite there, the 0 of an ignored row, is exact
+        tol = np.where(np.isnan(tol), 0, tol)
         d = np.where(fin, np.abs(got - ref) - np.where(fin, tol, 0), 0)
     assert d.max(initial=0) <= 0, (what, float(d.max()), np.unravel_index(d.argmax(), d.shape))
 
 
-def bounds(z, lse, T):
+def bounds(z, lse, T, threads=64):
     V = z.shape[1]
     with np.errstate(invalid="ignore", over="ignore"):
         s = z / T
@@ -44,12 +46,12 @@ def bounds(z, lse, T):
         p = np.exp(e) / np.exp(e).sum(1, keepdims=True)
         ae = np.where(p > 0, np.abs(e), 0)
         A, M2 = (p * ae).sum(1), (p * ae * ae).sum(1)
-        depth = V / 128 + 16
+        depth = V / (2 * threads) + 16   # two partial sums per thread of a row
         r = (3 * A + 4 + depth) * U
     return m, e, A, M2, depth, r
 
 
-def check(z, tokens, k=0, T=1.0, dev_logits=None):
+def check(z, tokens, k=0, T=1.0, dev_logits=None, threads=64):
     """z: CPU tensor [rows, V] in the stored dtype; dev_logits: the same values as the kernel gets them."""
     from decoder_only_transformer_causal_b200 import native
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -64,7 +66,7 @@ def check(z, tokens, k=0, T=1.0, dev_logits=None):
     assert int(status.item()) == 0
     z64 = f64(z)
     logp, ent, lse, ids, tlp = logprob_ref(z64, tokens.numpy(), k, T)
-    m, e, A, M2, depth, r = bounds(z64, lse, T)
+    m, e, A, M2, depth, r = bounds(z64, lse, T, threads)
     V = z64.shape[1]
     with np.errstate(invalid="ignore"):
         lv = 2 * math.log(V) * U
@@ -153,6 +155,39 @@ def test_special_rows(V, dtype):
     tok[2], tok[3], tok[12] = V // 2, V - 1, 3
     check(z.to(DT[dtype]), tok, min(V, 64))
     check(z.to(DT[dtype]), tok, 1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V,k", [
+    (1333, 1, 1), (1400, 31, 20), (1400, 127, 20), (1400, 300, 1), (1400, 1283, 20), (1400, 2557, 7), (1400, 4097, 0),
+    (1400, 5113, 1), (1333, 65, 40), (1400, 511, 40), (1400, 513, 21), (1500, 1030, 40), (1400, 5117, 20), (1400, 2051, 64),
+    (2800, 4100, 33), (1400, 10237, 3), (1332, 900, 20), (149, 16001, 2), (80, 16390, 9), (592, 28400, 5)])
+def test_rows_of_a_warp_or_two(rows, V, k, dtype):
+    """Sizes on both sides of where the number of threads per row changes; at least 32 of them."""
+    z, tok = make(rows, V, dtype)
+    check(z, tok, k, threads=32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V,ks", [(11, (1, 11)), (1237, (1, 20, 40)), (2563, (1, 20))])
+def test_special_values_in_many_rows(V, ks, dtype):
+    """Rows that keep, tie or lose everything, at more rows than run at once, each with another start."""
+    low = torch.finfo(DT[dtype]).min
+    z, tok = make(1408, V, dtype, banned=3)
+    z[0::11] = -math.inf
+    z[1::11] = low
+    z[2::11] = 2.5
+    z[3::11, V // 3] = math.nan
+    z[4::11, V // 2] = math.inf
+    z[5::11] = torch.randint(0, 3, z[5::11].shape, generator=torch.Generator().manual_seed(1)).to(DT[dtype])
+    z[6::11] = -math.inf; z[6::11, 2] = low
+    z[7::11] = (torch.arange(V) / 4096.0).to(DT[dtype])
+    tok[tok >= 0] %= V
+    buf = torch.full((1408 * (V + 1) + 9,), math.nan, dtype=DT[dtype], device="cuda")
+    x = buf[1:1 + 1408 * (V + 1)].view(1408, V + 1)[:, :V]
+    x.copy_(z)
+    for k in ks:
+        check(z, tok, k, 1.0, x, threads=32)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
