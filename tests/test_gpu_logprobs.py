@@ -322,6 +322,14 @@ def test_gradient_sizes(rows, V, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V", [(1300, 2057), (1200, 5121), (1190, 2563), (40, 9217), (5, 18440), (65600, 3)])
+def test_gradient_thread_counts(rows, V, dtype):
+    z, tok = make(rows, V, dtype, seed=5, banned=V // 9)
+    g = torch.Generator().manual_seed(V)
+    check_grad(z, tok, torch.randn(rows, generator=g), torch.randn(rows, generator=g), 1.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [0.3, 1.7, 1e3])
 def test_gradient_terms(T, dtype):
     z, tok = make(6, 777, dtype, seed=6)
