@@ -91,7 +91,15 @@ struct Slice {
     // f(value, column) over the elements of thread `first`.
     template <typename F>
     GPT_DEVINL void each(uint32_t first, F f) const {
-        for (uint32_t u = first; u < units; u += stride) unit(u, f);
+        uint32_t u = first;
+        for (; u + 3 * stride < units; u += 4 * stride) {
+            uint4 w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ldcg(reinterpret_cast<const uint4*>(z + unit_col(u + i * stride)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) values(w[i], unit_col(u + i * stride), f);
+        }
+        for (; u < units; u += stride) unit(u, f);
         if (first < ends) f(ld_act(z + end_col(first)), end_col(first));
     }
     template <typename F>
@@ -209,8 +217,9 @@ struct ScoreArgs {
 //
 // Top list.  The k-th largest of the CTA's thread maxima is a bound that at least k of its values
 // reach, and hardly more do: only the steps whose maximum reaches it (about k of them) are read
-// again, from L2.  More such values than places (long ties): a bisection over (value, index) finds a bound
-// that no more than fit reach.  12288 rows x 50257 bf16: 192 us without a list (6.4 TB/s), 206 with one
+// again, from L2.  More such values than places (long ties, masked rows with fewer than k tokens left): passes
+// over the row that halve the range of values in question, until few are left or all are equal, of which the
+// first count.  12288 rows x 50257 bf16: 192 us without a list (6.4 TB/s), 206 with one
 // entry, 226 with 20, 260 with 64.  The values' ranks among the candidates, and across CTAs by binary search in
 // the others' lists, are their places in the list.
 template <typename E, int NT>
@@ -219,7 +228,7 @@ logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
     constexpr uint32_t kPlaces = places(NT);
     griddep_launch_dependents();
     __shared__ float red[NT / 32], red_s[NT / 32], red_t[NT / 32];
-    __shared__ int ired[NT / 32];
+    __shared__ uint4 crowd[NT / 32];
     // the candidates lie where the slots were: shared memory is taken from the L1 that the loads in flight need
     // (9000 rows x 9001 bf16, 20 entries: 57.0 us with 10.9 KB per row of 64 threads, 52.5 with 6.8)
     __shared__ __align__(16) uint16_t slots[kSlots][NT];
@@ -420,27 +429,89 @@ logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
         __syncthreads();
         uint32_t count = s_count;
         if (count > kPlaces || n_hits > kPlaces) {
-            // the largest bound over (value, index) that at least k entries reach, bit by bit until few do
-            unsigned long long at_least = 0;
-            for (int bit = 63; bit >= 0; --bit) {
-                const unsigned long long at = at_least | (1ull << bit);
-                int above = 0;
-                row.each(first, [&](float z, uint32_t col) { above += entry(z, col) >= at; });
-                above = block_reduce<NT>(above, ired, [](int x, int y) { return x + y; });
-                if (above >= a.k) {
-                    at_least = at;
-                    if (above <= kPlaces) break;
+            // The crowd is cut down by passes that halve the keys in question, [lo, hi]: at least k values reach lo
+            // and n_above < k lie above hi.  Each pass also narrows the range to keys that occur, so that one
+            // value many times over (a masked row's -inf, a uniform row) is known after the first.  1000 rows x 50257
+            // bf16, 20 entries: 18 tokens left 125 us, a uniform row 75 (64 passes, one per bit of value and
+            // index, took 2130), against 29 for a row that needs none of this.
+            uint32_t lo = bound16 << 16, hi = 0xffffffffu, n_above = 0;
+            uint32_t mid = bound16 == 0 ? 0x00800000u : lo + 0x10000u;   // (first: the bound's own keys, or -inf, against those above)
+            if (bound16 == 0xffffu) lo = hi;
+            bool few = false;
+            while (lo < hi) {
+                uint32_t reach = 0, lowest = 0, below = 0, floor = 0;   // (the minima as maxima of ~key)
+                row.each(first, [&](float z, uint32_t) {
+                    const uint32_t key = order_key(z);
+                    if (key >= mid) {
+                        ++reach;
+                        lowest = max(lowest, ~key);
+                    } else if (key >= lo) {
+                        below = max(below, key);
+                        floor = max(floor, ~key);
+                    }
+                });
+                reach = __reduce_add_sync(0xffffffffu, reach);
+                lowest = __reduce_max_sync(0xffffffffu, lowest);
+                below = __reduce_max_sync(0xffffffffu, below);
+                floor = __reduce_max_sync(0xffffffffu, floor);
+                __syncthreads();
+                if (lane == 0) crowd[warp] = make_uint4(reach, lowest, below, floor);
+                __syncthreads();
+                uint4 c = crowd[0];
+#pragma unroll
+                for (int w = 1; w < NT / 32; ++w) {
+                    const uint4 o = crowd[w];
+                    c = make_uint4(c.x + o.x, max(c.y, o.y), max(c.z, o.z), max(c.w, o.w));
                 }
+                if (c.x >= static_cast<uint32_t>(a.k)) {
+                    lo = ~c.y;
+                    few = c.x <= kPlaces;
+                    if (few) break;
+                } else {
+                    n_above = c.x, hi = c.z, lo = ~c.w;
+                }
+                mid = lo + (hi - lo) / 2 + 1;
             }
+            // the values above, in any order; of those equal to lo the first in the order of the columns
             __syncthreads();
             if (tid == 0) s_count = 0;
             __syncthreads();
-            row.each(first, [&](float z, uint32_t col) {
-                const unsigned long long e = entry(z, col);
-                if (e >= at_least) cand[atomicAdd(&s_count, 1u)] = e;
-            });
+            if (few || n_above)
+                row.each(first, [&](float z, uint32_t col) {
+                    const uint32_t key = order_key(z);
+                    if (few ? key >= lo : key > lo) cand[atomicAdd(&s_count, 1u)] = entry(z, col);
+                });
+            if (!few && first < row.ends && order_key(z_end) == lo) cand[atomicAdd(&s_count, 1u)] = entry(z_end, row.end_col(first));
             __syncthreads();
             count = s_count;
+            const uint32_t need = few ? 0 : a.k - n_above;
+            uint32_t got = 0;
+            for (uint32_t u0 = rank * NT; u0 < row.units && got < need; u0 += row.stride) {
+                uint4 w = {};
+                uint32_t in = 0;
+                if (u0 + tid < row.units) {
+                    w = __ldcg(reinterpret_cast<const uint4*>(row.z + row.unit_col(u0 + tid)));
+                    row.values(w, 0, [&](float z, uint32_t e) { in |= static_cast<uint32_t>(order_key(z) == lo) << e; });
+                }
+                uint32_t at = __popc(in);   // up to and with this lane's
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const uint32_t before = __shfl_up_sync(0xffffffffu, at, o);
+                    if (lane >= o) at += before;
+                }
+                __syncthreads();
+                if (lane == 31) crowd[warp].x = at;
+                __syncthreads();
+                at += got - __popc(in);
+#pragma unroll
+                for (int x = 0; x < NT / 32; ++x) {
+                    if (x < warp) at += crowd[x].x;
+                    got += crowd[x].x;
+                }
+                for (; in && at < need; in &= in - 1, ++at)
+                    cand[count + at] = static_cast<unsigned long long>(lo) << 32 | (0xffffffffu - (row.unit_col(u0 + tid) + __ffs(in) - 1));
+            }
+            count += min(got, need);
         }
         // places by counting
         const uint32_t padded = (count + 7) & ~7u;   // (at most kPlaces)
@@ -713,15 +784,16 @@ int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int
     // 12.4 / 17.6 / 23.2, 64: 13.4 / 27.3 / 32.1, 128: 19.1 / 36.0 / 40.7; 9000 x 5000 bf16: 25.5 / 31.7 / 37.8,
     // 23.2 / 36.6 / 41.7, 30.2 / 48.1 / 52.5; 9000 x 9001 fp32: 66.3 / 72.9 / 92.7, 56.7 / 68.7 / 73.9, 60.0 / 80.9 /
     // 84.9.  Long rows want enough CTAs for several waves as well: 2000 x 32000 bf16: 64 threads 30.1 / 34.2 / 35.7,
-    // 128: 27.9 / 33.0 / 34.6; 12288 x 50257: 191.8 / 205.7 / 226, 193.7 / 214.1 / 227, 40 entries 253 and 242.  The list's bound needs more threads than entries: 64 threads with 64 entries fall
-    // back to the bisection (8805 x 2057: 195 against 58 us).
+    // 128: 27.9 / 33.0 / 34.6; 12288 x 50257: 191.8 / 205.7 / 226, 193.7 / 214.1 / 227, 40 entries 253 and 242.  The list's
+    // bound needs more threads than entries: 64 threads with 64 entries pass over a crowd (8805 x 2057 bf16:
+    // 40 entries 41 against 48 us with 128 threads, 48: 49 and 51, 56: 65 and 56, 64: 179 and 59).
     // At most four rows per SM: twice the loads in flight once a row or all of them are long (592 x 50257 bf16:
     // 256 threads 15.0 / 18.0 / 18.5, 128: 17.6 / 20.3 / 20.8; 300 rows: 11.4 / 14.2 / 14.7, 9.8 / 12.4 / 12.9).
     const long long row_units = (static_cast<long long>(V) * (dtype == GPT_DTYPE_BF16 ? 2 : 4) + 15) / 16;
     a.threads = 128;
     if (cluster > 1 || (rows <= 148 && row_units >= 2048) || (rows <= 148 * 4 && rows * row_units >= 1 << 21)) a.threads = 256;
     else if (rows > 148 * 9 && k <= 20 && row_units <= (k ? 640 : 512)) a.threads = 32;
-    else if (rows > 148 * 9 && k <= 40 && (row_units <= 1280 || (k <= 20 && 2ll * rows >= 3 * row_units))) a.threads = 64;
+    else if (rows > 148 * 9 && k <= 40 && (row_units <= 1280 || (k <= 32 && 2ll * rows >= 3 * row_units))) a.threads = 64;
     const long long step = static_cast<long long>(a.threads) * cluster * kUnroll * (dtype == GPT_DTYPE_BF16 ? 8 : 4);
     while ((V + step - 1) / step > static_cast<long long>(kSlots) << a.slot_shift) ++a.slot_shift;
     return dtype == GPT_DTYPE_BF16 ? launch_score(static_cast<const bf16*>(logits), a, rows, s)

@@ -191,6 +191,24 @@ def test_special_values_in_many_rows(V, ks, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,V,k", [(6, 50257, 64), (6, 4099, 20), (160, 20011, 40), (700, 1501, 64), (1400, 1501, 20), (1400, 1501, 40), (2, 131, 64)])
+def test_fewer_values_than_entries(rows, V, k, dtype):
+    """Rows whose mask leaves fewer tokens than entries are asked for, rows of one or two values, and rows whose
+    upper half lies within a 256th of one value; equal values are listed by index."""
+    z, tok = make(rows, V, dtype)
+    g = torch.Generator().manual_seed(V)
+    order = torch.rand((rows, V), generator=g).argsort(1).argsort(1)
+    left = torch.tensor([0, 1, k - 1, k, k // 2, V])[torch.arange(rows) % 6]
+    z[order >= left[:, None]] = -math.inf
+    z[3::6] = (torch.arange(V) >= V - 5).to(DT[dtype])            # few ones, behind
+    z[4::6] = (torch.arange(V) % 97 == 96).to(DT[dtype]) * -2.0   # ones apart: ties in the order of the columns
+    z[5::6, V // 2:] = (100.0 + torch.rand((z[5::6].shape[0], V - V // 2), generator=g) * 0.3).to(DT[dtype])
+    low = torch.finfo(DT[dtype]).min
+    z[0::12, ::2] = low                                           # nothing but the lowest value and -inf
+    check(z, torch.where(tok >= 0, order.argmin(1), tok), k, threads=32)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_crowded_top(dtype):
     """Many more values at or above the k-th largest of any partition than a short list holds."""
     V = 50257
