@@ -64,6 +64,8 @@ GPT_DEVINL bool elect_one() {
     return r != 0;
 }
 
+GPT_DEVINL float4 sum(const float4& a, const float4& b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); }
+
 // Parts of a softmax over disjoint keys: weighted values o (eight of a row), {maximum (log2 units), sum}.
 // A part without keys has a sum of 0 and its o is not looked at.
 struct Joined {
@@ -142,10 +144,21 @@ GPT_DEVINL void load_tree(const TreeArgs& a, int b, bool report, int* par, unsig
 //   S [128 x 128] = Q' K^T, Q' the R = 32 or 64 node rows repeated 128 / R times, so that the 128 TMEM
 //     lanes are 128 / R groups of all nodes; group g uses the columns [g R, (g + 1) R) of its rows only:
 //     every thread has R scores, a row of its own, and no reduction between threads;
-//   O [128 x 64] += P V, P block-diagonal (group g's lanes hold 0 outside its columns, written once), so
-//     one chain of products accumulates every group's share, joined at the end.
+//   O [128 x 64] += P V, one chain of products for the shares of all groups, joined at the end.
 // The repeated rows cost tensor time (2 cycles per key of the 11 that its bytes take at this GPU's copy
 // rate) and save the transposes and shuffles that splitting the keys over lanes would take.
+//
+// A bf16 operand holds 8 bits of a weight that was computed in 32, so a weight p enters the product as
+// hi + lo: hi its upper 16 bits, lo the rest rounded to bf16, off by at most 2^-15 p.  hi and lo have a lane each and
+// their rows of O are added at the end, so that the tensor cores do no more than for hi alone:
+//   N <= 16 (TWICE): a group has 16 nodes' rows twice; both lanes compute p, one hands on hi and one lo;
+//   else groups 2 k and 2 k + 1 keep a running maximum together and exchange half of their weights' parts through
+//     shared memory: the lanes of 2 k hold hi of both groups' columns, those of 2 k + 1 lo.
+// P is 0 in the columns that are not a lane's (written once).  Against p rounded to bf16 (2-norm error 1.7e-3 to
+// 2.3e-3; now 1.5e-3 to 1.7e-3, the rounding of y alone), us in a burst / back to back: 8 sequences x 16 nodes x 12
+// heads 13.0 / 13.0 -> 13.4 / 13.5, 48 x 23 x 25 up to 8185 keys 244 / 277 -> 253 / 293, 32 x 64 x 16 up to 4096 keys
+// 55.5 / 63.6 -> 65.5 / 76.4.  Two products per tile instead, lo's behind hi's: 281 / 333 and 66 / 78.  For N > 32
+// eight warps with half of the columns each: 66 / 78.
 //
 // The nodes' own keys lie in the last R rows of the last tile, behind the cache's rest if that leaves room.
 //
@@ -160,8 +173,9 @@ GPT_DEVINL void load_tree(const TreeArgs& a, int b, bool report, int* par, unsig
 namespace tc {
 constexpr int HS = 64;
 constexpr int KEYS = 128;
-constexpr int BOX = 32;                       // rows per load of the nodes' q, k, v and of the cache's rest
-constexpr int BOX_BYTES = BOX * HS * 2;
+constexpr int BOX = 32;                       // rows per load of the cache's rest
+constexpr int node_box(bool twice) { return twice ? 16 : 32; }   // ... and of the nodes' q, k, v
+constexpr int ROW_BYTES = HS * 2;
 constexpr int THREADS = 192;
 constexpr int TILE = KEYS * HS * 2;           // 16 KB
 constexpr int HALF = HS / 2, HALF_LD = HALF + 4;   // the groups' parts are joined half a row at a time
@@ -174,6 +188,7 @@ struct Tail {
     uint64_t q_full, q_empty, k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES], s_free, p_full, drain;
     unsigned long long see[kMaxNodes], bad;   // bad: node rows of V with values that are not finite
     float2 ml[KEYS], joined_ml[kMaxNodes];
+    float mx[KEYS];
     int par[kMaxNodes];
     int lengths[THREADS];                     // with longest_first: in the order of the pairs,
     short order[THREADS];                     // and the sequences they belong to
@@ -211,11 +226,12 @@ GPT_DEVINL Work work_of(int pair, const TreeArgs& a, const Tail& T, int rank, in
     return w;
 }
 
-template <int R>
+template <int R, bool TWICE>
 __global__ void __launch_bounds__(THREADS, 2)
     tree_attention_tc(const __grid_constant__ CUtensorMap tmNode, const __grid_constant__ CUtensorMap tmCache,
                       const __grid_constant__ CUtensorMap tmRest, const bf16* __restrict__ qkv, bf16* __restrict__ y,
                       const TreeArgs a) {
+    constexpr int ROWS = TWICE ? R / 2 : R, NODE_BOX = node_box(TWICE);
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t* sQ = smem;
@@ -291,11 +307,11 @@ __global__ void __launch_bounds__(THREADS, 2)
                             return;
                         }
                         const int boxes = (w.rest + BOX - 1) / BOX;
-                        mbar_arrive_expect_tx(full, (boxes + R / BOX) * BOX_BYTES);
+                        mbar_arrive_expect_tx(full, (boxes * BOX + R) * ROW_BYTES);
                         for (int i = 0; i < boxes; ++i)
-                            tma_load_4d(dst + i * BOX_BYTES, &tmRest, full, 0, v * a.nh + w.h, t * KEYS + i * BOX, w.b);
-                        for (int i = 0; i < R / BOX; ++i)
-                            tma_load_4d(dst + ((KEYS - R) / BOX + i) * BOX_BYTES, &tmNode, full, 0, (1 + v) * a.nh + w.h, i * BOX, w.b);
+                            tma_load_4d(dst + i * BOX * ROW_BYTES, &tmRest, full, 0, v * a.nh + w.h, t * KEYS + i * BOX, w.b);
+                        for (int i = 0; i < R; i += NODE_BOX)
+                            tma_load_4d(dst + (KEYS - R + i) * ROW_BYTES, &tmNode, full, 0, (1 + v) * a.nh + w.h, i, w.b);
                     };
                     if (!(ok = mbar_wait(&T.k_empty[st], ph ^ 1u, abort_flag))) break;
                     tile(0);
@@ -306,8 +322,8 @@ __global__ void __launch_bounds__(THREADS, 2)
                             break;
                         }
                         mbar_arrive_expect_tx(&T.q_full, TILE);
-                        for (int i = 0; i < KEYS / BOX; ++i)
-                            tma_load_4d(sQ + i * BOX_BYTES, &tmNode, &T.q_full, 0, w.h, (i * BOX) % R, w.b);
+                        for (int i = 0; i < KEYS; i += NODE_BOX)
+                            tma_load_4d(sQ + i * ROW_BYTES, &tmNode, &T.q_full, 0, w.h, i % ROWS, w.b);
                         ++n_q;
                     }
                     if (!mbar_wait(&T.v_empty[st], ph ^ 1u, abort_flag)) {
@@ -386,7 +402,10 @@ __global__ void __launch_bounds__(THREADS, 2)
         // ------------------------------------------------------------ softmax and join
         const int t = threadIdx.x - 64;
         const int quarter = warp & 3;
-        const int r = quarter * 32 + lane, group = r / R, node = r % R, col0 = group * R;
+        const int r = quarter * 32 + lane, group = r / R, node = r % R, col0 = group * R;   // node: of key row r
+        // the pair of groups that share their weights, and the warps that hold it
+        const int odd = group & 1, pair_bar = 2 + (R == 64 ? quarter & 1 : quarter >> 1);
+        uint4* swap = reinterpret_cast<uint4*>(sPart);
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + COL_S + lane_off + col0, tP = tmem + COL_P + lane_off, tO = tmem + COL_O + lane_off;
         const bool node_group = group == KEYS / R - 1;
@@ -420,7 +439,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                 if (w.h == 0 && rank == 0 && t < a.N && T.see[t] == 0 && T.par[t] != -2) set_status(a.status, GPT_ERR_INDEX);
             }
             named_barrier(1, 128);
-            const unsigned long long see = T.see[node];
+            const unsigned long long see = T.see[r % ROWS], see_key = T.see[node];
             float m_used = -INFINITY, l = 0.f;
             for (int j = 0; j < w.n_steps; ++j, ++n) {
                 const bool last = w.last(j);
@@ -431,7 +450,7 @@ __global__ void __launch_bounds__(THREADS, 2)
                     const bool got = mbar_wait(&T.v_full[st], (n / STAGES) & 1, abort_flag);
                     uint4* row = reinterpret_cast<uint4*>(sV + st * TILE + r * (HS * 2));
                     const bool is_node = last && node_group;
-                    if (got && (is_node ? see == 0 : r >= keys)) {
+                    if (got && (is_node ? see_key == 0 : r >= keys)) {
 #pragma unroll
                         for (int i = 0; i < HS / 8; ++i) row[i] = make_uint4(0, 0, 0, 0);
                     } else if (got && is_node) {
@@ -452,23 +471,25 @@ __global__ void __launch_bounds__(THREADS, 2)
                     }
                     fence_proxy_async_shared();
                 }
-                const bool got = mbar_wait(&T.k_empty[st], (n / STAGES) & 1, abort_flag);   // K_n read: S_n is there
-                __syncwarp();   // tcgen05.ld / st are warp-collective
-                if (!__all_sync(0xffffffffu, got)) {
+                // K_n read: S_n is there
+                const bool got = __all_sync(0xffffffffu, mbar_wait(&T.k_empty[st], (n / STAGES) & 1, abort_flag));
+                if (TWICE && !got) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
                 float s[R];
-                {
+                if (got) {   // (tcgen05.ld / st are warp-collective)
+                    tc_fence_after();
                     uint32_t u[R];
                     if constexpr (R == 32) tmem_ld32(tS, u);
                     else tmem_ld64(tS, u);
 #pragma unroll
                     for (int c = 0; c < R; ++c) s[c] = __uint_as_float(u[c]);
                 }
-                tc_fence_before();
-                mbar_arrive(&T.s_free);
+                if (got) {
+                    tc_fence_before();
+                    mbar_arrive(&T.s_free);
+                }
                 if (last && node_group) {
 #pragma unroll
                     for (int c = 0; c < R; ++c)
@@ -481,7 +502,15 @@ __global__ void __launch_bounds__(THREADS, 2)
                 float m4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
                 for (int c = 4; c < R; ++c) m4[c & 3] = fmaxf(m4[c & 3], s[c]);
-                const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.scale_log2;
+                if constexpr (!TWICE) {   // ... of both groups; a time-out of one warp ends the steps of its partner as well
+                    T.mx[r] = mx;
+                    if (named_barrier_or(pair_bar, 64, !got)) {
+                        ok = false;
+                        break;
+                    }
+                    mx = fmaxf(mx, T.mx[r ^ R]);
+                }
                 float alpha = 1.f;
                 if (mx > m_used + kRescaleThreshold || (m_used == -INFINITY && mx > -INFINITY)) {
                     alpha = m_used == -INFINITY ? 0.f : exp2_approx(m_used - mx);
@@ -490,31 +519,57 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const float off = m_used == -INFINITY ? 0.f : -m_used;   // nothing visible yet: 2^-inf
                 const uint64_t sc2 = f2_pack(a.scale_log2, a.scale_log2), off2 = f2_pack(off, off);
                 uint64_t acc[2] = {0, 0};
-                uint32_t pk[R / 2];
+                uint32_t hi[R / 2], lo[R / 2];
 #pragma unroll
                 for (int c = 0; c < R; c += 2) {
                     float x0, x1;
                     f2_unpack(f2_fma(f2_pack(s[c], s[c + 1]), sc2, off2), x0, x1);
                     const float p0 = exp2_approx(x0), p1 = exp2_approx(x1);
                     acc[(c >> 1) & 1] = f2_add(acc[(c >> 1) & 1], f2_pack(p0, p1));
-                    pk[c / 2] = pack_bf16x2(p0, p1);
+                    // (hi is cut, not rounded: lo need not wait for a conversion; 69 us with it, 65.5 without)
+                    const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+                    hi[c / 2] = __byte_perm(b0, b1, 0x7632);
+                    float r0, r1;
+                    f2_unpack(f2_sub(f2_pack(p0, p1), f2_pack(__uint_as_float(b0 & 0xffff0000u), __uint_as_float(b1 & 0xffff0000u))), r0, r1);
+                    lo[c / 2] = pack_bf16x2(r0, r1);
                 }
                 float a0, a1;
                 f2_unpack(f2_add(acc[0], acc[1]), a0, a1);
                 l = l * alpha + (a0 + a1);
                 // P_n may overwrite P_{n-1} and O may be rescaled only after O += P_{n-1} V_{n-1} (for a
                 // pair's first step the join before it has waited for that).
-                if (j > 0) {
-                    const bool done = mbar_wait(&T.v_empty[(n - 1) % STAGES], ((n - 1) / STAGES) & 1, abort_flag);
-                    __syncwarp();
-                    if (!__all_sync(0xffffffffu, done)) {
-                        ok = false;
-                        break;
-                    }
+                auto p_free = [&]() {
+                    if (j == 0) return true;
+                    const bool done = __all_sync(0xffffffffu, mbar_wait(&T.v_empty[(n - 1) % STAGES], ((n - 1) / STAGES) & 1, abort_flag));
                     tc_fence_after();
+                    return done;
+                };
+                if constexpr (TWICE) {
+#pragma unroll
+                    for (int c = 0; c < R / 2; ++c)
+                        if (r & ROWS) hi[c] = lo[c];
+                    ok = p_free();
+                    if (ok) tmem_st_nowait(tP + group * (R / 2), hi);
+                } else {
+                    auto exchange = [&](const uint32_t(&mine)[R / 2], uint32_t(&other)[R / 2]) {
+#pragma unroll
+                        for (int c = 0; c < R / 2; c += 4)
+                            swap[c * (KEYS / 4) + r] = make_uint4(other[c], other[c + 1], other[c + 2], other[c + 3]);
+                        const bool done = p_free();
+                        if (done) tmem_st_nowait(tP + group * (R / 2), mine);
+                        if (named_barrier_or(pair_bar, 64, !done)) return false;
+#pragma unroll
+                        for (int c = 0; c < R / 2; c += 4) {
+                            const uint4 v = swap[c * (KEYS / 4) + (r ^ R)];
+                            other[c] = v.x, other[c + 1] = v.y, other[c + 2] = v.z, other[c + 3] = v.w;
+                        }
+                        tmem_st_nowait(tP + (group ^ 1) * (R / 2), other);
+                        return true;
+                    };
+                    ok = odd ? exchange(lo, hi) : exchange(hi, lo);
                 }
-                if constexpr (R == 32) tmem_st16(tP + group * (R / 2), pk);
-                else tmem_st32(tP + group * (R / 2), pk);
+                tmem_wait_st();
+                if (!ok) break;
                 if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
 #pragma unroll
                     for (int c = 0; c < HS; c += 32) {
@@ -547,15 +602,22 @@ __global__ void __launch_bounds__(THREADS, 2)
                 const unsigned long long bad = T.bad;
                 for (int it = t; it < a.N << pieces_log2; it += 128) {
                     const int i = it >> pieces_log2, dp = (it & ((1 << pieces_log2) - 1)) * 8, d = d0 + dp;
-                    float2 ml[KEYS / R];
+                    // rows (2 ROWS) g + i and ROWS further: the same weights' hi and lo, or two groups' shares of them
+                    constexpr int PARTS = KEYS / (2 * ROWS);
+                    float2 ml[PARTS];
                     Joined x;
 #pragma unroll
-                    for (int g = 0; g < KEYS / R; ++g) ml[g] = T.ml[g * R + i], x.see(ml[g]);
+                    for (int g = 0; g < PARTS; ++g) {
+                        ml[g] = T.ml[2 * ROWS * g + i];
+                        if constexpr (!TWICE) ml[g].y += T.ml[2 * ROWS * g + ROWS + i].y;
+                        x.see(ml[g]);
+                    }
 #pragma unroll
-                    for (int g = 0; g < KEYS / R; ++g)
+                    for (int g = 0; g < PARTS; ++g)
                         if (ml[g].y != 0.f) {
-                            const float4* o = reinterpret_cast<const float4*>(part + (g * R + i) * ld + dp);
-                            x.add(ml[g], o[0], o[1]);
+                            const float4* o = reinterpret_cast<const float4*>(part + (2 * ROWS * g + i) * ld + dp);
+                            const float4* lo = reinterpret_cast<const float4*>(part + (2 * ROWS * g + ROWS + i) * ld + dp);
+                            x.add(ml[g], sum(o[0], lo[0]), sum(o[1], lo[1]));
                         }
                     if (a.cluster > 1) {
                         st8(joined + i * LD + d, x.o);
@@ -1069,15 +1131,15 @@ int launch_tree_attention(int dtype, const void* qkv, const void* kv, const int*
                : hs <= 64 ? f32::launch<2>(node_map, cache_map, qkv, y, a, grid.x, s)
                           : f32::launch<4>(node_map, cache_map, qkv, y, a, grid.x, s);
     }
-    const uint32_t node_box[4] = {64, 1, tc::BOX, 1}, cache_box[4] = {64, 1, tc::KEYS, 1}, rest_box[4] = {64, 1, tc::BOX, 1};
+    const bool twice = N <= 16;
+    const uint32_t node_box[4] = {64, 1, static_cast<uint32_t>(tc::node_box(twice)), 1}, cache_box[4] = {64, 1, tc::KEYS, 1}, rest_box[4] = {64, 1, tc::BOX, 1};
     rc = make_tmap_bf16_4d(&node_map, qkv, node_dims, node_strides, node_box);
     if (!rc) rc = make_tmap_bf16_4d(&cache_map, kv, cache_dims, cache_strides, cache_box);
     if (!rc) rc = make_tmap_bf16_4d(&rest_map, kv, cache_dims, cache_strides, rest_box);
     if (rc) return rc;
-    static size_t opted32[kMaxDevices] = {}, opted64[kMaxDevices] = {};
-    auto kern = N <= 32 ? tc::tree_attention_tc<32> : tc::tree_attention_tc<64>;
-    rc = N <= 32 ? opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted32)
-                 : opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted64);
+    static size_t opted[3][kMaxDevices] = {};
+    auto kern = twice ? tc::tree_attention_tc<32, true> : N <= 32 ? tc::tree_attention_tc<32, false> : tc::tree_attention_tc<64, false>;
+    rc = opt_in_smem(reinterpret_cast<const void*>(kern), tc::SMEM, opted[twice ? 0 : N <= 32 ? 1 : 2]);
     if (rc) return rc;
     return launch_overlapped_cluster(kern, a.cluster, grid, dim3(tc::THREADS), tc::SMEM, s, node_map, cache_map, rest_map,
                                      static_cast<const bf16*>(qkv), static_cast<bf16*>(y), a);

@@ -343,8 +343,8 @@ int gpt_generate(const gpt_config_t* cfg, const void* weights, const int64_t* id
  * from lengths[b] on and other branches' k and v may hold any value, NaN included.
  *   qkv     [B, N, 3, nh * hs]; kv [B, block_size, 2, nh * hs]; y [B, N, nh * hs] (no overlap with
  *           the inputs); all in `dtype`, 16-byte aligned.
- *   GPT_DTYPE_BF16: hs 64 (fp32 scores, statistics and sums; the probabilities are rounded to bf16 as
- *           operands of the product with v).  GPT_DTYPE_F32: hs % 8 == 0, hs <= 128 (every product of two
+ *   GPT_DTYPE_BF16: hs 64 (fp32 scores, statistics and sums; a probability enters the product with v to
+ *           2^-15 of it, as two bf16 numbers).  GPT_DTYPE_F32: hs % 8 == 0, hs <= 128 (every product of two
  *           fp32 numbers to 5 x 2^-22 of it, as three TF32 products; fp32 sums).
  *   N = 1 with parent -1 is the attention of an ordinary decode step with a length per sequence.
  *   status  optional device int32 (NULL allowed), never cleared by the library.

@@ -228,6 +228,31 @@ def test_tree_attention_calls_at_once(dtype):
     assert all(torch.equal(y, want[i]) for i in range(2) for y in got[i])
 
 
+@pytest.mark.parametrize("B,N,nh,cap,lens", [
+    (1, 1, 12, 1024, [700]), (3, 1, 2, 300, [0, 65, 300]), (2, 16, 12, 1024, [1000, 3]), (5, 17, 2, 257, [256, 255, 257, 0, 31]),
+    (4, 23, 5, 515, [515, 514, 192, 191]), (3, 32, 4, 130, [130, 32, 0]), (4, 33, 2, 300, [0, 128, 300, 5]),
+    (4, 64, 2, 700, [700, 640, 64, 0]), (1, 64, 1, 5000, [4999]), (70, 3, 16, 130, [(13 * i) % 131 for i in range(70)]),
+    (40, 20, 16, 300, [(77 * i) % 301 for i in range(40)]), (40, 50, 12, 300, [(77 * i) % 301 for i in range(40)])])
+@pytest.mark.parametrize("qscale", [0.3, 3.0])
+def test_tree_attention_keeps_the_weights_bits(B, N, nh, cap, lens, qscale):
+    """bf16: a weight is off by 2^-15 of itself (its upper 16 bits and the rest, off by half a step, 2^-8, of at most
+    2^-7 of it), where one bf16 number would be off by 2^-8; everything else as in the tolerance above."""
+    from decoder_only_transformer_causal_b200 import native
+    g = torch.Generator().manual_seed(cap + N)
+    qkv = torch.randn((B, N, 3, nh * 64), generator=g)
+    qkv[:, :, 0] *= qscale
+    qkv = qkv.to(torch.bfloat16)
+    kv = torch.randn((B, cap, 2, nh * 64), generator=g).to(torch.bfloat16)
+    par = random_parents(B, N, seed=N)
+    y = f64(native.tree_attention(qkv.cuda(), kv.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), torch.tensor(par).cuda(), nh))
+    q64, kv64 = f64(qkv), f64(kv)
+    ref, a = tree_attention_ref(q64, kv64, lens, par, nh)
+    tol = attn_tol(q64, kv64, lens, nh, np.zeros_like(ref), a, "f32") + 2.0 ** -15 * a     # of the sums
+    tol += 2.0 ** -8 * (np.abs(ref) + tol)                                                 # of the result's rounding
+    err = np.abs(y - ref)
+    assert (err <= tol).all(), (float((err - tol).max()), float(err.max()), np.unravel_index((err - tol).argmax(), err.shape))
+
+
 # ------------------------------------------------------------------ the model over a tree
 def tree_model(name, layers, B, T0, **over):
     from decoder_only_transformer_causal_b200 import GPT, GPTConfig, native
