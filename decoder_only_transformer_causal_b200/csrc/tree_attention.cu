@@ -744,7 +744,7 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint4* sQ = reinterpret_cast<uint4*>(ring + 2 * STAGES * P * PANEL);   // [step][node tile][hi, lo][lane]
     __shared__ unsigned long long see[kMaxNodes], s_bad;
-    __shared__ uint64_t full[STAGES], empty[STAGES];
+    __shared__ uint64_t full[STAGES], empty[STAGES], never;   // nothing arrives on never
     __shared__ int par[kMaxNodes];
     __shared__ float2 ml[2][ROWS], joined_ml[ROWS];
     __shared__ int s_abort;
@@ -759,6 +759,7 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
     const float* node = qkv + static_cast<long long>(b) * N * 3 * C + h * hs;
     if (tid == 0) {
         for (int st = 0; st < STAGES; ++st) mbar_init(&full[st], 1), mbar_init(&empty[st], 4 * NG);
+        mbar_init(&never, 1);
         s_abort = 0;
         s_bad = 0;
         fence_barrier_init();
@@ -772,8 +773,10 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
     const int len = clamp_length(__ldcg(a.lengths + b), a.block_size, h == 0 && rank == 0 && tid == 0 ? a.status : nullptr);
     const int n_cache = (len + KEYS - 1) / KEYS;   // tile n_cache is the nodes'
     const int n_panels = (hs + 31) / 32;
+    int issued = 0;   // tiles whose copies the loading thread has issued: one after another, round the stages
     auto load_tile = [&](int t, int stage) {   // one thread
         if (t > n_cache) return;
+        ++issued;
         mbar_arrive_expect_tx(&full[stage], 2 * n_panels * PANEL);
         for (int v = 0; v < 2; ++v)
             for (int p = 0; p < n_panels; ++p) {
@@ -823,8 +826,12 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
                 for (int e = 0; e < 4; ++e) o[mt][p][q][e] = 0.f;
     }
     const int key0 = key_warp * 16;
+    // After a wait that gave up, a warp still goes through the remaining tiles (the others may wait for it at a
+    // barrier), on whatever the stages hold, but arrives on nothing, so that the loading thread issues no more.
     bool ok = true;
-    int n = 0;   // tiles taken
+    // Testing aid (gpt_set_wait_limit_ns): with the first loads under way, no tile is waited for.
+    if (g_force_timeout && tid < THREADS) ok = mbar_wait(&never, 0, abort_flag);
+    int n = 0;   // tiles gone through
     if (tid >= THREADS) {
         if (lane == 0) {
             for (int t = rank; t <= n_cache; t += a.cluster, ++n) {
@@ -970,18 +977,18 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
         }
         fence_proxy_async_shared();   // what was read and cleared here before what the next copies write
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
+        if (lane == 0 && ok) mbar_arrive(&empty[stage]);
         if (NG > 1 && tid == LOADER && t + STAGES * a.cluster <= n_cache) {
-            ok = mbar_wait(&empty[stage], (n / STAGES) & 1, abort_flag) && ok;
+            ok = ok && mbar_wait(&empty[stage], (n / STAGES) & 1, abort_flag);
             if (ok) load_tile(t + STAGES * a.cluster, stage);
         }
         __syncwarp();
     }
-    if (!ok) {   // no bulk copy may still target shared memory when the CTA exits
-        for (int i = 1; tid < THREADS && i <= STAGES && i <= n; ++i) mbar_drain(&full[(n - i) % STAGES], ((n - i) / STAGES) & 1);
-        set_status(a.status, GPT_ERR_TIMEOUT);
-    }
+    // No bulk copy may still target shared memory when it is used again below, or when the CTA exits.
+    if (tid == LOADER)
+        for (int i = 1; i <= STAGES && i <= issued; ++i) mbar_drain(&full[(issued - i) % STAGES], ((issued - i) / STAGES) & 1);
     __syncthreads();
+    if (tid == 0 && *abort_flag) set_status(a.status, GPT_ERR_TIMEOUT);
 
     // In the ring's place: the first and third key warp leave their parts, the second and fourth join theirs to
     // them, then the two, then the CTAs'.

@@ -147,3 +147,39 @@ def test_tree_attention_wait_limit_gives_timeout_then_recovers(short_waits, N):
         mask = torch.ones((N, n + N), dtype=torch.bool, device="cuda").tril(n)
         ref = torch.nn.functional.scaled_dot_product_attention(q, x[:, 0].transpose(0, 1), x[:, 1].transpose(0, 1), attn_mask=mask)
         assert float((y[b].float() - ref.transpose(0, 1).reshape(N, 128)).abs().max()) <= 2e-2
+
+
+# B, N, heads, head size, cache, lengths: one to three loads per CTA or many, with and without a cluster, both ways
+# of loading (a warp of its own up to 32 nodes, a thread of the products beyond), whole and cut tiles
+F32_TREES = [(2, 20, 2, 64, 1000, [1000, 130]), (2, 64, 2, 64, 1000, [1000, 130]), (60, 5, 16, 64, 700, [700 - 11 * i for i in range(60)]),
+             (60, 40, 8, 32, 700, [700 - 11 * i for i in range(60)]), (40, 17, 12, 128, 300, [7 * i for i in range(40)]), (1, 3, 1, 8, 64, [0])]
+
+
+@pytest.mark.parametrize("B,N,nh,hs,cap,lens", F32_TREES)
+def test_fp32_tree_attention_wait_limit_gives_timeout_then_recovers(short_waits, B, N, nh, hs, cap, lens):
+    """The warps of the products give up with the first copies under way: all leave together, the copies that were
+    issued land, and the next call is undisturbed."""
+    native = short_waits
+    g = torch.Generator(device="cuda").manual_seed(74)
+    qkv = torch.randn((B, N, 3, nh * hs), generator=g, device="cuda")
+    kv = torch.randn((B, cap, 2, nh * hs), generator=g, device="cuda")
+    lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    par = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.tree_attention(qkv, kv, lens, par, nh, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_ERR_TIMEOUT
+    native.set_wait_limit_ns(0)
+    st.zero_()
+    y = native.tree_attention(qkv, kv, lens, par, nh, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_OK
+    for b in (0, B // 2, B - 1):                         # a chain: the tail of causal attention
+        n = int(lens[b])
+        x = torch.cat([kv[b, :n], qkv[b, :, 1:]]).double().view(n + N, 2, nh, hs)
+        q = qkv[b, :, 0].double().view(N, nh, hs).transpose(0, 1)
+        mask = torch.ones((N, n + N), dtype=torch.bool, device="cuda").tril(n)
+        s = (q @ x[:, 0].permute(1, 2, 0) * hs ** -0.5).masked_fill(~mask, -float("inf"))
+        ref = (torch.softmax(s, -1) @ x[:, 1].transpose(0, 1)).transpose(0, 1).reshape(N, nh * hs)
+        # 2 a ((hs + 28) u D + (n + N + 28) u) of test_gpu_tree's tolerance with hs 128, D 10, n 1100, a 1
+        assert float((y[b] - ref).abs().max()) <= 4e-4
