@@ -81,8 +81,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 1) {
         tmem_alloc(tmem_slot, 32);
         tmem_relinquish();
+        griddep_launch_dependents();   // not before: a dependent could hold the columns that this warp waits for
     }
-    griddep_launch_dependents();
     griddep_wait();
 
     // The producer's sequence of loads: this CTA's tiles in turn, each as num_kb 128 x 64 boxes.

@@ -265,8 +265,8 @@ __global__ void __launch_bounds__(THREADS, 2)
     if (warp == 1) {
         tmem_alloc(&T.tmem, TMEM_COLS);
         tmem_relinquish();
+        griddep_launch_dependents();   // not before: a dependent could hold the columns that this warp waits for
     }
-    griddep_launch_dependents();
     griddep_wait();
     if (a.longest_first) {   // the sequences in the order of their lengths, equal ones by index
         const int t = threadIdx.x;
