@@ -619,14 +619,14 @@ struct GradArgs {
 struct RowGrad {
     float inv_t, L, g, h, gh;
     GPT_DEVINL uint64_t two(float a, float b) const {
-        // -inf: 2^-1e30 = 0, and l stays finite
-        uint64_t l = f2_fma(f2_pack(a, b), f2_pack(inv_t, inv_t), f2_pack(-L, -L));
-        float l0, l1;
-        f2_unpack(l, l0, l1);
-        l = f2_pack(fmaxf(l0, -1e30f), fmaxf(l1, -1e30f));
+        const uint64_t l = f2_fma(f2_pack(a, b), f2_pack(inv_t, inv_t), f2_pack(-L, -L));
+        float l0, l1, v0, v1;
         f2_unpack(f2_mul(l, f2_pack(1.4426950408889634f, 1.4426950408889634f)), l0, l1);
+        const float p0 = exp2_approx(l0), p1 = exp2_approx(l1);
         const uint64_t w = f2_fma(f2_pack(h, h), l, f2_pack(gh, gh));
-        return f2_mul(f2_pack(-exp2_approx(l0), -exp2_approx(l1)), w);
+        f2_unpack(f2_mul(f2_pack(-p0, -p1), w), v0, v1);
+        // where p is 0 so is the gradient, whatever the factors' size makes of l = -inf or far below 0
+        return f2_pack(p0 == 0.f ? 0.f : v0, p1 == 0.f ? 0.f : v1);
     }
     GPT_DEVINL float one(float z, bool hit) const {
         float v, unused;

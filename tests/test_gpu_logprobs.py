@@ -432,3 +432,21 @@ def test_forward_backward_against_differences():
         # differences: eps^2 times a third derivative of order 100; rounding 1e-15 * 100 / eps.
         # gradient: entries off by about 1e-6 of themselves (tolerances above), 1800 of them
         assert abs(num - float((d * w).sum())) <= 1e-6 + 4e-6 * np.abs(d * w).sum()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("h,T", [(1.0, 1.0), (4e8, 1.0), (1.0, 2e-9), (2.0 ** 20, 1e-3), (-3e9, 0.5), (1e30, 1.0), (1e20, 1e-12)])
+@pytest.mark.parametrize("V,doff", [(1003, 0), (1003, 1), (50304, 0)])
+def test_gradient_of_forbidden_tokens_is_zero_at_any_factor(V, doff, h, T, dtype):
+    """Logits of -inf, and those so far below the maximum that their probability is 0, get 0 however large the
+    entropy's factor over the temperature is."""
+    g = torch.Generator().manual_seed(V)
+    z = torch.randint(0, 2, (4, V), generator=g).to(DT[dtype]) * (-1.0 if T < 1e-2 else 0.25)
+    z[:, ::3] = -math.inf
+    z[1, 1::3] = -200.0
+    z[2, 1:] = -math.inf; z[2, 0] = 0.0                          # one token left: its gradient is 0 as well
+    z[3, 1:] = torch.finfo(DT[dtype]).min; z[3, 0] = 0.0
+    tok = torch.tensor([1, 2, 0, -1])
+    buf = torch.full((doff + 4 * V,), 42.0, dtype=DT[dtype], device="cuda")
+    d = check_grad(z, tok, torch.ones(4), torch.full((4,), h), T, out=buf[doff:].view(4, V))
+    assert (d[:2, ::3] == 0).all() and (d[1, 1::3] == 0).all() and (d[2:] == 0).all()
