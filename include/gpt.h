@@ -338,8 +338,9 @@ int gpt_generate(const gpt_config_t* cfg, const void* weights, const int64_t* id
 /* Attention of the nodes over the cache and their ancestors:
  *   y[b, i, h] = sum_j softmax_j(q[b, i, h] . k_j / sqrt(hs)) v_j,
  *   j over cached positions [0, lengths[b]) and A(i).
- * Rows with no node are written as zeros.  A visible k or v that is not finite leaves NaN or an infinity in
- * what it reaches.  What a row does not see cannot change it: cached positions
+ * Rows with no node are written as zeros.  A visible v that is not finite leaves NaN or an infinity in
+ * its dimension of the rows that see it, a visible k NaN in all of its head (or, where it makes the score
+ * -inf, weight 0).  What a row does not see cannot change it: cached positions
  * from lengths[b] on and other branches' k and v may hold any value, NaN included.
  *   qkv     [B, N, 3, nh * hs]; kv [B, block_size, 2, nh * hs]; y [B, N, nh * hs] (no overlap with
  *           the inputs); all in `dtype`, 16-byte aligned.

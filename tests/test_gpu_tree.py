@@ -253,6 +253,50 @@ def test_tree_attention_keeps_the_weights_bits(B, N, nh, cap, lens, qscale):
     assert (err <= tol).all(), (float((err - tol).max()), float(err.max()), np.unravel_index((err - tol).argmax(), err.shape))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("N", [9, 20, 64])
+@pytest.mark.parametrize("B,nh,cap", [(2, 2, 400), (30, 12, 300)])
+def test_tree_attention_nodes_with_values_that_are_not_numbers(B, nh, cap, N, dtype):
+    """A node's key or value that is NaN or infinite reaches the rows that see the node, in the value's dimensions
+    (a key: in all of its head), and leaves every other bit as it is: with clusters (few pairs) and without, for
+    nodes below and above the 32nd."""
+    from decoder_only_transformer_causal_b200 import native
+    par = random_parents(B, N, 3)
+    lens = [(77 * i + 300) % (cap + 1) for i in range(B)]
+    y, _, (qkv, kv, l, p) = run_attention(B, N, nh, 64, cap, lens, par, dtype, seed=N, poison=False)
+    sees = see_sets(par)
+    inf, nan = float("inf"), float("nan")
+
+    def compare(bad, want):
+        y2 = native.tree_attention(bad, kv, l, p, nh)
+        both = torch.isnan(want) & torch.isnan(y2)
+        assert torch.equal(torch.where(both, 0, y2), torch.where(both, 0, want))
+
+    for first in (1, N // 2, N - 4):             # values: one node, then another with the opposite infinity
+        bad, want = qkv.clone(), y.clone()
+        for b in range(B):
+            for node, vals in ((first, (inf, -inf, nan)), (0, (0, inf, -inf))):
+                for i in range(N):
+                    if node in sees[b][i]:
+                        for d, v in zip((3, 40, 63), vals):
+                            want[b, i, 64 * (nh - 1) + d] += v if v else 0
+                for d, v in zip((3, 40, 63), vals):
+                    if v:
+                        bad[b, node, 2, 64 * (nh - 1) + d] = v
+        compare(bad, want)
+        bad, want = qkv.clone(), y.clone()       # keys: NaN, and an infinity that every query meets with its sign
+        bad[:, :, 0, 5] = bad[:, :, 0, 5].abs() + 0.5
+        y3 = native.tree_attention(bad, kv, l, p, nh)
+        for key in (nan, inf):
+            bad[:, first, 1, 5] = key
+            want = y3.clone()
+            for b in range(B):
+                for i in range(N):
+                    if first in sees[b][i]:
+                        want[b, i, :64] = nan
+            compare(bad, want)
+
+
 # ------------------------------------------------------------------ the model over a tree
 def tree_model(name, layers, B, T0, **over):
     from decoder_only_transformer_causal_b200 import GPT, GPTConfig, native
