@@ -99,15 +99,12 @@ class GPT:
         root, -2 for no node) over the cache's first lengths int32 [B] positions, takes the likeliest token at
         each node, and keeps the path that the choices confirm (its k, v go into the cache).  Returns
         (native.TreeAccept, chosen int64 [B, N]); the kept tokens are chosen along the path.  Calls of a model
-        share its workspace and node buffers: order them on one stream."""
+        share its workspace: order them on one stream."""
         B, N = tok.shape
-        key = ("tree", B, N)
-        if key not in self._host:
-            self._host[key] = native.alloc_tree_qkv(self.cfg, B, N, self.device)
-        logits = native.tree_step(self.cfg, self.weights, tok, parents, lengths, kv_cache, self._host[key],
-                                  self.workspace(B, N))
+        tree_qkv = native.alloc_tree_qkv(self.cfg, B, N, self.device)
+        logits = native.tree_step(self.cfg, self.weights, tok, parents, lengths, kv_cache, tree_qkv, self.workspace(B, N))
         chosen = native.token_logprobs(logits.view(B * N, -1), None, k=1).top_ids.view(B, N)
-        return native.tree_accept(self.cfg, parents, tok, chosen, lengths, self._host[key], kv_cache), chosen
+        return native.tree_accept(self.cfg, parents, tok, chosen, lengths, tree_qkv, kv_cache), chosen
 
 
 class AdamW:

@@ -529,3 +529,20 @@ def test_model_calls():
     # a log probability moves by at most twice what the logits do
     assert max_abs(f64(r.logp), ref) <= 2 * F32_ATOL and r.top_ids.shape == (3, 20, 4)
     assert max_abs(f64(r.entropy), -(np.exp(lp) * lp).sum(-1)) <= 2 * F32_ATOL * (1 + np.abs(lp).max())
+
+
+def test_verify_keeps_no_buffers():
+    """Batches and draft widths that vary leave nothing behind but the model's workspace."""
+    B, T0 = 4, 10
+    m, cfg, _, _, kv = tree_model("tiny", None, B, T0)
+
+    def verify(B, N):
+        par = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+        m.verify(torch.ones((B, N), dtype=torch.int64, device="cuda"), par, torch.full((B,), T0, dtype=torch.int32, device="cuda"), kv)
+        torch.cuda.synchronize()
+    verify(B, 12)
+    held = torch.cuda.memory_allocated()
+    for b in range(1, B + 1):
+        for n in range(1, 13):
+            verify(b, n)
+    assert torch.cuda.memory_allocated() == held
