@@ -270,6 +270,16 @@ def check_status(workspace: torch.Tensor, stream=None) -> int:
     return LIB.gpt_check_status(_ptr(workspace), _stream(stream))
 
 
+def raise_status(workspace: torch.Tensor, where: str, stream=None) -> None:
+    """check_status, raising on anything but GPT_OK."""
+    _check(check_status(workspace, stream), where)
+
+
+def status_word(workspace: torch.Tensor) -> torch.Tensor:
+    """A workspace's status word, as the status argument of the calls that have no workspace."""
+    return workspace[:4].view(torch.int32)
+
+
 def set_wait_limit_ns(ns: int, force_timeout: bool = False) -> None:
     """gpt_set_wait_limit_ns: the pipeline-wait limit of the tensor-core kernels on the current
     device (0 restores the default) and the forced time-out; a testing aid for the time-out path."""

@@ -546,3 +546,37 @@ def test_verify_keeps_no_buffers():
         for n in range(1, 13):
             verify(b, n)
     assert torch.cuda.memory_allocated() == held
+
+
+def test_verify_and_score_report_what_is_wrong():
+    from decoder_only_transformer_causal_b200 import native
+    m, cfg, _, _, kv = tree_model("tiny", None, 1, 20)
+    chain = [-1, 0, 1, 2]
+
+    def verify(tok, par, length, **kw):
+        return m.verify(torch.tensor([tok]).cuda(), torch.tensor([par], dtype=torch.int32).cuda(),
+                        torch.tensor([length], dtype=torch.int32).cuda(), kv, **kw)
+    verify([1, 2, 3, 4], chain, 20, sync_check=True)
+    for tok, par, length, code in (([1, 65, 3, 4], chain, 20, native.GPT_ERR_INDEX), ([1, 2, -1, 4], chain, 20, native.GPT_ERR_INDEX),
+                                   ([1, 2, 3, 4], [-1, 0, 2, 1], 20, native.GPT_ERR_INDEX), ([1, 2, 3, 4], chain, -1, native.GPT_ERR_BAD_SHAPE),
+                                   ([1, 2, 3, 4], chain, 65, native.GPT_ERR_BAD_SHAPE)):
+        with pytest.raises(native.GPTError) as e:
+            verify(tok, par, length, sync_check=True)
+        assert e.value.status == code, (tok, par, length)
+        verify(tok, par, length)
+        assert native.check_status(m.workspace(1, 4)) == code
+    verify([1, 2, 3, 4], chain, 20, sync_check=True)              # an error is not kept for the next call
+
+    idx, tgt = torch.randint(0, 65, (2, 9)), torch.randint(0, 65, (2, 9))
+    tgt[0, 3] = -1
+    m.score(idx.cuda(), tgt.cuda(), k=2, sync_check=True)
+    for i, t in ((idx, 65), (idx, -1), (tgt, 65), (tgt, -2)):
+        keep = i[1, 4].item()
+        i[1, 4] = t
+        with pytest.raises(native.GPTError) as e:
+            m.score(idx.cuda(), tgt.cuda(), k=2, sync_check=True)
+        assert e.value.status == native.GPT_ERR_INDEX, t
+        m.score(idx.cuda(), tgt.cuda())
+        assert native.check_status(m.workspace(2, 9)) == native.GPT_ERR_INDEX
+        i[1, 4] = keep
+    m.score(idx.cuda(), tgt.cuda(), sync_check=True)
