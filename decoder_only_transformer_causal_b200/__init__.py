@@ -85,34 +85,45 @@ class GPT:
         return native.generate(self.cfg, self.weights, idx, max_new_tokens, uniforms, temperature, top_k,
                                kv_cache=self._host[key], workspace=ws, step_logits=step_logits)
 
+    def _vocab(self, vocab: int | None) -> int:
+        if vocab is None:
+            return self.cfg.vocab_size
+        if not 1 <= vocab <= self.cfg.vocab_size:
+            raise ValueError(f"vocab must be in [1, {self.cfg.vocab_size}], got {vocab}")
+        return vocab
+
     def score(self, idx: torch.Tensor, targets: torch.Tensor, k: int = 0, temperature: float = 1.0,
-              sync_check: bool = False):
+              vocab: int | None = None, sync_check: bool = False):
         """Log probabilities of targets int64 [B, T] (-1: not scored) after idx [B, T], with each position's
         entropy and, for k > 0, its k likeliest tokens: a native.TokenLogprobs of [B, T] (and [B, T, k])
-        tensors.  sync_check: wait, and raise if a token or target was out of range (else they are in
-        native.check_status(model.workspace(B, T)))."""
+        tensors.  vocab: how many of the model's columns are tokens, where its vocabulary is padded (default:
+        all); the others have no probability.  sync_check: wait, and raise if a token or target was out of
+        range (else that is in native.check_status(model.workspace(B, T)))."""
         B, T = idx.shape
+        vocab = self._vocab(vocab)
         ws = self.workspace(B, T)
         logits, _ = self(idx, targets)
-        r = native.token_logprobs(logits.view(B * T, -1), targets.reshape(-1), k=k, temperature=temperature,
+        r = native.token_logprobs(logits.view(B * T, -1)[:, :vocab], targets.reshape(-1), k=k, temperature=temperature,
                                   status=native.status_word(ws))
         if sync_check:
             native.raise_status(ws, "GPT.score")
         return native.TokenLogprobs(*(None if t is None else t.view(B, T, *t.shape[1:]) for t in r))
 
     def verify(self, tok: torch.Tensor, parents: torch.Tensor, lengths: torch.Tensor, kv_cache: torch.Tensor,
-               sync_check: bool = False):
+               vocab: int | None = None, sync_check: bool = False):
         """One greedy step over drafted trees: runs the nodes tok int64 [B, N] (parents int32 [B, N], -1 for a
         root, -2 for no node) over the cache's first lengths int32 [B] positions, takes the likeliest token at
         each node, and keeps the path that the choices confirm (its k, v go into the cache).  Returns
         (native.TreeAccept, chosen int64 [B, N]); the kept tokens are chosen along the path.  Calls of a model
-        share its workspace: order them on one stream.  sync_check: wait, and raise if a token, parent or length
+        share its workspace: order them on one stream.  vocab: how many of the model's columns are tokens
+        to choose from (default: all, as in generate).  sync_check: wait, and raise if a token, parent or length
         was out of range (else that is in native.check_status(model.workspace(B, N)))."""
         B, N = tok.shape
+        vocab = self._vocab(vocab)
         ws, tree_qkv = self.workspace(B, N), native.alloc_tree_qkv(self.cfg, B, N, self.device)
         status = native.status_word(ws)   # cleared by tree_step
         logits = native.tree_step(self.cfg, self.weights, tok, parents, lengths, kv_cache, tree_qkv, ws)
-        chosen = native.token_logprobs(logits.view(B * N, -1), None, k=1).top_ids.view(B, N)
+        chosen = native.token_logprobs(logits.view(B * N, -1)[:, :vocab], None, k=1).top_ids.view(B, N)
         accepted = native.tree_accept(self.cfg, parents, tok, chosen, lengths, tree_qkv, kv_cache, status=status)
         if sync_check:
             native.raise_status(ws, "GPT.verify")

@@ -580,3 +580,36 @@ def test_verify_and_score_report_what_is_wrong():
         assert native.check_status(m.workspace(2, 9)) == native.GPT_ERR_INDEX
         i[1, 4] = keep
     m.score(idx.cuda(), tgt.cuda(), sync_check=True)
+
+
+def test_verify_and_score_of_a_padded_vocabulary():
+    """Columns behind the last token are neither chosen nor counted."""
+    from decoder_only_transformer_causal_b200 import native
+    B, T0, N = 2, 10, 5
+    m, cfg, _, prompt, kv = tree_model("tiny", None, B, T0)
+    par = torch.tensor([[-1, 0, 1, 0, 3]] * B, dtype=torch.int32, device="cuda")
+    tok = torch.randint(0, 65, (B, N), generator=torch.Generator().manual_seed(1)).cuda()
+    lens = torch.full((B,), T0, dtype=torch.int32, device="cuda")
+    kv2, tq = kv.clone(), native.alloc_tree_qkv(m.cfg, B, N)
+    logits = native.tree_step(m.cfg, m.weights, tok, par, lens, kv2, tq, m.workspace(B, N))
+    real = int(logits.argmax(-1).max())                           # the last of the likeliest is padding
+    assert real > 1
+    acc, chosen = m.verify(tok, par, lens, kv, vocab=real, sync_check=True)
+    assert torch.equal(chosen, logits[..., :real].argmax(-1))
+    want = native.tree_accept(m.cfg, par, tok, chosen, lens, tq, kv2)
+    assert all(torch.equal(a, b) for a, b in zip(acc, want)) and torch.equal(kv, kv2)
+
+    idx, tgt = (t % real for t in seeded.make_tokens(3, 20, 65, seed=77))
+    r = m.score(idx.cuda(), tgt.cuda(), k=4, vocab=real, sync_check=True)
+    z = f64(m(idx.cuda(), tgt.cuda())[0])[..., :real]
+    lp = z - np.log(np.exp(z - z.max(-1, keepdims=True)).sum(-1, keepdims=True)) - z.max(-1, keepdims=True)
+    # logits of the same kernels: what is left are fp32 roundings of values below 32 (2^-24 * 32, four of them)
+    assert max_abs(f64(r.logp), np.take_along_axis(lp, tgt.numpy()[..., None], -1)[..., 0]) <= 2.0 ** -17
+    assert max_abs(f64(r.entropy), -(np.exp(lp) * lp).sum(-1)) <= 2.0 ** -17 and int(r.top_ids.max()) < real
+    with pytest.raises(native.GPTError):                          # a target in the padding
+        m.score(idx.cuda(), torch.full_like(tgt, real).cuda(), vocab=real, sync_check=True)
+    for bad in (0, -1, 66):
+        with pytest.raises(ValueError):
+            m.score(idx.cuda(), tgt.cuda(), vocab=bad)
+        with pytest.raises(ValueError):
+            m.verify(tok, par, lens, kv, vocab=bad)
