@@ -724,6 +724,12 @@ GPT_DEVINL void split_cut(float x, uint32_t& hi, uint32_t& lo) {
     hi = __float_as_uint(x) & 0xffffe000u;
     lo = tf32(x - __uint_as_float(hi));
 }
+// Queries: hi rounded, but cut where the type's largest values would round to infinity (there lo is 2^-11 of x as well).
+GPT_DEVINL void split_finite(float x, uint32_t& hi, uint32_t& lo) {
+    hi = tf32(x);
+    if ((hi & 0x7f800000u) == 0x7f800000u) hi = __float_as_uint(x) & 0xffffe000u;
+    lo = tf32(x - __uint_as_float(hi));
+}
 GPT_DEVINL void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
     asm(
         "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
@@ -801,7 +807,7 @@ __global__ void __launch_bounds__(block_threads(NG), NG > 1 || P > 2 ? 1 : MT > 
         for (int e = 0; e < 2; ++e) {
             const int i = row + e * 8;
             const float2 q = i < N && dim < hs ? __ldcg(reinterpret_cast<const float2*>(node + i * 3 * C + dim)) : make_float2(0.f, 0.f);
-            split(q.x, hi[e], lo[e]), split(q.y, hi[e + 2], lo[e + 2]);
+            split_finite(q.x, hi[e], lo[e]), split_finite(q.y, hi[e + 2], lo[e + 2]);
         }
         sQ[((s * MT * NG + tile) * 2) * 32 + l] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         sQ[((s * MT * NG + tile) * 2 + 1) * 32 + l] = make_uint4(lo[0], lo[1], lo[2], lo[3]);

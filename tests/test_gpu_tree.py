@@ -169,6 +169,26 @@ def test_tree_attention_values_that_are_not_numbers():
         assert torch.equal(y2, y)
 
 
+@pytest.mark.parametrize("dtype,hs", [("bf16", 64), ("f32", 64), ("f32", 8), ("f32", 128)])
+@pytest.mark.parametrize("N", [5, 20, 50])
+def test_tree_attention_largest_queries(N, dtype, hs):
+    """Queries of the type's largest values against keys that are 0 or tiny there: scores are ordinary numbers."""
+    from decoder_only_transformer_causal_b200 import native
+    B, nh, cap, lens, par = 3, 2, 300, [300, 77, 0], random_parents(3, N, 3)
+    g = torch.Generator().manual_seed(N)
+    qkv, kv = torch.randn((B, N, 3, nh * hs), generator=g), torch.randn((B, cap, 2, nh * hs), generator=g)
+    sign = torch.randint(0, 2, (B, N, nh), generator=g) * 2.0 - 1
+    qkv, kv = qkv.to(DT[dtype]), kv.to(DT[dtype])
+    qkv[:, :, 0, 1::hs] = (sign * torch.finfo(DT[dtype]).max).to(DT[dtype])
+    qkv[:, :, 1, 1::hs] = (torch.randint(-1, 2, (B, N, nh), generator=g) * 2.0 ** -123).to(DT[dtype])
+    kv[:, :, 0, 1::hs] = (torch.randint(-1, 2, (B, cap, nh), generator=g) * 2.0 ** -123).to(DT[dtype])
+    y = f64(native.tree_attention(qkv.cuda(), kv.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), torch.tensor(par).cuda(), nh))
+    q64, kv64 = f64(qkv), f64(kv)
+    ref, a = tree_attention_ref(q64, kv64, lens, par, nh)
+    tol = attn_tol(q64, kv64, lens, nh, ref, a, dtype)
+    assert (np.abs(y - ref) <= tol).all(), float(np.abs(y - ref).max())
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("N", [1, 40])
 def test_tree_attention_offsets_past_32_bits(N, dtype):
