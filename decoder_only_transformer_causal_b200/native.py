@@ -666,6 +666,8 @@ def _rows(name: str, t: torch.Tensor, like: torch.Tensor):
     if t is not like and (t.shape != like.shape or t.dtype is not like.dtype or t.device != like.device):
         raise ValueError(f"{name} must have the logits' shape, dtype and device")
     rows, V = t.shape
+    if rows > 0x7fffffff or V > 0x7fffffff:
+        raise ValueError(f"{name}: at most 2^31 - 1 rows and columns")
     ld, one = t.stride()
     if V > 1 and one != 1:
         raise ValueError(f"{name}: the entries of a row must be contiguous")

@@ -146,6 +146,15 @@ def test_python_argument_checks():
         native.token_logprobs(z.double())
 
 
+@pytest.mark.parametrize("shape", [(2 ** 32 + 5, 1), (2 ** 31, 2), (1, 2 ** 32 + 100), (3, 2 ** 31)])
+def test_sizes_past_the_calls_integers_are_refused(shape):
+    z = torch.empty(shape, dtype=torch.bfloat16, device="meta")
+    with pytest.raises(ValueError, match="at most"):
+        native.token_logprobs(z)
+    with pytest.raises(ValueError, match="at most"):
+        native.token_logprobs_backward(z, None, torch.empty(shape[0], device="meta"))
+
+
 # ------------------------------------------------------------------ the definitions themselves
 def test_see_sets():
     par = np.array([[-1, 0, 0, 1, 3, -2, 5, 9, -1, 8]])
