@@ -152,13 +152,12 @@ GPT_DEVINL void load_tree(const TreeArgs& a, int b, bool report, int* par, unsig
 // hi + lo: hi its upper 16 bits, lo the rest rounded to bf16, off by at most 2^-15 p.  hi and lo have a lane each and
 // their rows of O are added at the end, so that the tensor cores do no more than for hi alone:
 //   N <= 16 (TWICE): a group has 16 nodes' rows twice; both lanes compute p, one hands on hi and one lo;
-//   else groups 2 k and 2 k + 1 keep a running maximum together and exchange half of their weights' parts through
-//     shared memory: the lanes of 2 k hold hi of both groups' columns, those of 2 k + 1 lo.
+//   else groups 2 k and 2 k + 1 keep a running maximum together, and a lane has hi of its own columns and lo of the
+//     other group's, which come through shared memory.
 // P is 0 in the columns that are not a lane's (written once).  Against p rounded to bf16 (2-norm error 1.7e-3 to
 // 2.3e-3; now 1.5e-3 to 1.7e-3, the rounding of y alone), us in a burst / back to back: 8 sequences x 16 nodes x 12
-// heads 13.0 / 13.0 -> 13.4 / 13.5, 48 x 23 x 25 up to 8185 keys 244 / 277 -> 253 / 293, 32 x 64 x 16 up to 4096 keys
-// 55.5 / 63.6 -> 65.5 / 76.4.  Two products per tile instead, lo's behind hi's: 281 / 333 and 66 / 78.  For N > 32
-// eight warps with half of the columns each: 66 / 78.
+// heads 13.0 / 13.0 -> 13.5 / 13.5, 48 x 23 x 25 up to 8185 keys 244 / 278 -> 253 / 292, 32 x 64 x 16 up to 4096 keys
+// 56 / 64 -> 63 / 73.5.  Two products per tile instead, lo's behind hi's: 281 / 333 and 66 / 78.
 //
 // The nodes' own keys lie in the last R rows of the last tile, behind the cache's rest if that leaves room.
 //
@@ -404,7 +403,7 @@ __global__ void __launch_bounds__(THREADS, 2)
         const int quarter = warp & 3;
         const int r = quarter * 32 + lane, group = r / R, node = r % R, col0 = group * R;   // node: of key row r
         // the pair of groups that share their weights, and the warps that hold it
-        const int odd = group & 1, pair_bar = 2 + (R == 64 ? quarter & 1 : quarter >> 1);
+        const int pair_bar = 2 + (R == 64 ? quarter & 1 : quarter >> 1);
         uint4* swap = reinterpret_cast<uint4*>(sPart);
         const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
         const uint32_t tS = tmem + COL_S + lane_off + col0, tP = tmem + COL_P + lane_off, tO = tmem + COL_O + lane_off;
@@ -551,22 +550,19 @@ __global__ void __launch_bounds__(THREADS, 2)
                     ok = p_free();
                     if (ok) tmem_st_nowait(tP + group * (R / 2), hi);
                 } else {
-                    auto exchange = [&](const uint32_t(&mine)[R / 2], uint32_t(&other)[R / 2]) {
 #pragma unroll
-                        for (int c = 0; c < R / 2; c += 4)
-                            swap[c * (KEYS / 4) + r] = make_uint4(other[c], other[c + 1], other[c + 2], other[c + 3]);
-                        const bool done = p_free();
-                        if (done) tmem_st_nowait(tP + group * (R / 2), mine);
-                        if (named_barrier_or(pair_bar, 64, !done)) return false;
+                    for (int c = 0; c < R / 2; c += 4) swap[c * (KEYS / 4) + r] = make_uint4(lo[c], lo[c + 1], lo[c + 2], lo[c + 3]);
+                    ok = p_free();
+                    if (ok) tmem_st_nowait(tP + group * (R / 2), hi);
+                    ok = !named_barrier_or(pair_bar, 64, !ok);
+                    if (ok) {
 #pragma unroll
                         for (int c = 0; c < R / 2; c += 4) {
                             const uint4 v = swap[c * (KEYS / 4) + (r ^ R)];
-                            other[c] = v.x, other[c + 1] = v.y, other[c + 2] = v.z, other[c + 3] = v.w;
+                            lo[c] = v.x, lo[c + 1] = v.y, lo[c + 2] = v.z, lo[c + 3] = v.w;
                         }
-                        tmem_st_nowait(tP + (group ^ 1) * (R / 2), other);
-                        return true;
-                    };
-                    ok = odd ? exchange(lo, hi) : exchange(hi, lo);
+                        tmem_st_nowait(tP + (group ^ 1) * (R / 2), lo);
+                    }
                 }
                 tmem_wait_st();
                 if (!ok) break;
