@@ -219,9 +219,9 @@ struct ScoreArgs {
 // reach, and hardly more do: only the steps whose maximum reaches it (about k of them) are read
 // again, from L2.  More such values than places (long ties, masked rows with fewer than k tokens left): passes
 // over the row that halve the range of values in question, until few are left or all are equal, of which the
-// first count.  12288 rows x 50257 bf16: 192 us without a list (6.4 TB/s), 206 with one
-// entry, 226 with 20, 260 with 64.  The values' ranks among the candidates, and across CTAs by binary search in
-// the others' lists, are their places in the list.
+// first count.  12288 rows x 50257 bf16, in a burst / back to back (power cap): without a list 192 / 207 us (6.4 TB/s),
+// one entry 205 / 221, 20 entries 229 / 240, 32 entries 248 / 250.  The values' ranks among the candidates, and across
+// CTAs by binary search in the others' lists, are their places in the list.
 template <typename E, int NT>
 __global__ void __launch_bounds__(NT, NT > 128 ? 4 : NT == 32 ? 32 : (sizeof(E) == 2 ? 9 : 8) * 128 / NT)
 logprobs_kernel(const E* __restrict__ logits, const ScoreArgs a) {
@@ -642,7 +642,7 @@ GPT_DEVINL uint4 grad_unit(const RowGrad& q, const uint4& w, uint32_t hit, const
     for (int i = 0; i < 4; ++i) {
         float a, b;
         f2_unpack(q.two(__uint_as_float(x[i] << 16), __uint_as_float(x[i] & 0xffff0000u)), a, b);
-        if (hit < 8) {   // the token's column is one of these nine (bf16) or eight (fp32)
+        if (hit < 8) {   // the token's column is one of these eight
             if (hit == 2 * i) a += q.g;
             if (hit == 2 * i + 1) b += q.g;
         }
@@ -783,10 +783,14 @@ int launch_logprobs(const void* logits, long long ld, const int64_t* tokens, int
     // the same however many threads it has, so that short rows want few.  9000 rows x 2057 bf16: 32 threads
     // 12.4 / 17.6 / 23.2, 64: 13.4 / 27.3 / 32.1, 128: 19.1 / 36.0 / 40.7; 9000 x 5000 bf16: 25.5 / 31.7 / 37.8,
     // 23.2 / 36.6 / 41.7, 30.2 / 48.1 / 52.5; 9000 x 9001 fp32: 66.3 / 72.9 / 92.7, 56.7 / 68.7 / 73.9, 60.0 / 80.9 /
-    // 84.9.  Long rows want enough CTAs for several waves as well: 2000 x 32000 bf16: 64 threads 30.1 / 34.2 / 35.7,
-    // 128: 27.9 / 33.0 / 34.6; 12288 x 50257: 191.8 / 205.7 / 226, 193.7 / 214.1 / 227, 40 entries 253 and 242.  The list's
-    // bound needs more threads than entries: 64 threads with 64 entries pass over a crowd (8805 x 2057 bf16:
-    // 40 entries 41 against 48 us with 128 threads, 48: 49 and 51, 56: 65 and 56, 64: 179 and 59).
+    // 84.9.  The list's bound needs more threads than entries: 64 threads with 64 entries pass over a crowd (8805 x
+    // 2057 bf16: 40 entries 41 against 48 us with 128 threads, 48: 49 and 51, 56: 65 and 56, 64: 179 and 59).
+    // Long rows want enough CTAs for several waves as well (us with 0 / 1 / 20 / 32 alternatives, 64 threads | 128),
+    // from 3 rows per 2 units on: 12288 x 50257 bf16 192 / 205 / 229 / 248 | 194 / 231 / 236 / 242, 9000 x 32000 99 /
+    // 116 / 118 / 126 | 95 / 124 / 123 / 120, 6000 x 20000 47 / 56 / 61 / 64 | 45 / 62 / 62 / 65, 9000 x 12000 fp32 69 / 87 / 89 /
+    // 93 | 74 / 98 / 99 / 102, 13000 x 32003 255 / 277 / 293 / 305 | 252 / 284 / 295 / 303; below: 3000 x 32000 bf16 43 / 49 / 52 / 53 | 39 /
+    // 46 / 48 / 50, 2500 x 20000 24 / 28 / 29 / 30 | 23 / 28 / 30 / 31, 3000 x 12000 fp32 30 / 36 / 38 / 40 | 29 / 36 / 38 / 40; 8000 x
+    // 50257 bf16 (2.5 rows per 2 units) and 4000 x 32003 fp32 (1) lie within 6% of one another, either way.
     // At most four rows per SM: twice the loads in flight once a row or all of them are long (592 x 50257 bf16:
     // 256 threads 15.0 / 18.0 / 18.5, 128: 17.6 / 20.3 / 20.8; 300 rows: 11.4 / 14.2 / 14.7, 9.8 / 12.4 / 12.9).
     const long long row_units = (static_cast<long long>(V) * (dtype == GPT_DTYPE_BF16 ? 2 : 4) + 15) / 16;
@@ -805,8 +809,10 @@ int launch_logprobs_backward(const void* logits, long long ld, const int64_t* to
                              const float* dentropy, void* dlogits, long long ldd, int32_t* status, cudaStream_t s) {
     const GradArgs a = {ld, ldd, tokens, static_cast<uint32_t>(V), 1.f / temperature, lse, entropy, dlogp, dentropy, status};
     // a CTA takes at least 4 units per thread; rows are split only while there are fewer than 8 CTAs per SM
-    // Threads per CTA, from the 16-byte units of a row (us with 64 / 128 / 256): 9000 rows x 2057 bf16 15.0 / 17.4 /
-    // 26.9, x 5000 bf16 32.1 / 33.9 / 41.0, x 9001 bf16 55.0 / 54.1 / 60.5, x 20000 bf16 118.8 / 114.9 / 112.5
+    // Threads per CTA, from the 16-byte units of a row (us with 64 / 128 / 256).  Logits and gradient aligned alike: 9000
+    // rows x 2057 bf16 15.6 / 16.9 / 25.8, x 5000 32.2 / 34.6 / 41.3, x 9001 55.5 / 55.6 / 62.0, x 18001 106.8 / 104.0 /
+    // 103.6, x 27001 161 / 155 / 151; differently: 19.7 / 21.6 / 27.8, 51.0 / 53.4 / 63.7, 84 / 86 / 88, 151 / 155 / 163,
+    // 227 / 226 / 218.  fp32 9000 x 5000 60.3 / 60.6 / 67.9 and 77.9 / 78.0 / 84.9, 4000 x 32003 180 / 170 / 163 and 207 / 207 / 197
     const long long row_units = (static_cast<long long>(V) * (dtype == GPT_DTYPE_BF16 ? 2 : 4) + 15) / 16;
     const int threads = row_units <= 640 ? 64 : row_units <= 2304 ? 128 : kThreads;
     const int per = threads * kUnroll * (dtype == GPT_DTYPE_BF16 ? kVec<bf16> : kVec<float>);

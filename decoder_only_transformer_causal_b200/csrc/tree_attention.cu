@@ -484,8 +484,6 @@ __global__ void __launch_bounds__(THREADS, 2)
                     else tmem_ld64(tS, u);
 #pragma unroll
                     for (int c = 0; c < R; ++c) s[c] = __uint_as_float(u[c]);
-                }
-                if (got) {
                     tc_fence_before();
                     mbar_arrive(&T.s_free);
                 }
@@ -681,7 +679,10 @@ __global__ void __launch_bounds__(THREADS, 2)
 // ---------------------------------------------------------------- fp32, head size 8 to 128
 // The same split with fp32 operands: every product of two fp32 numbers is taken as three TF32 products
 // (x = hi + lo, TF32 each; hi hi + hi lo + lo hi, fp32 accumulation), off by at most 5 x 2^-22 of it (the
-// product of the two lo, 2^-10 and 2^-11 of their numbers, and the roundings of each lo).
+// product of the two lo, 2^-10 and 2^-11 of their numbers, and the roundings of each lo).  The refinement is that of
+// S. Markidis et al., "NVIDIA Tensor Core Programmability, Performance & Precision" (IPDPSW 2018); that the products'
+// accumulator is cut and needs short chains, of H. Ootomo and R. Yokota, "Recovering single precision accuracy from
+// Tensor Cores while surpassing the FP32 theoretical peak performance" (IJHPCA 2022).
 //
 // Tiles of 64 keys come by TMA (panels of 32 dimensions, 128-byte swizzle), two in flight.  A warp has 16 of a
 // tile's keys and 16 MT nodes (NG groups of four warps take the nodes of up to 64): each K and V element is
@@ -692,7 +693,8 @@ __global__ void __launch_bounds__(THREADS, 2)
 // Against CUDA-core tiles of 2 x 4 scores per thread, which shared-memory reads bind: 19 / 26 us (8 sequences
 // x 9 nodes x 12 heads of 64, up to 1013 keys), 68 / 84 us (32 x 30 x 12 of 64, 700 keys), 352 / 545 us
 // (20 x 50 x 16 of 128, 2000 keys).  The TF32 products bind it from about 32 nodes on (mma.sync: a 16 x 8 x 8
-// product took about 16 cycles per scheduler), their latency below.
+// product took about 16 cycles per scheduler), their latency below.  With two node tiles per warp registers spill
+// (bytes stored, as ptxas counts them, for P, MT, NG): 2, 2, 1: 160; 4, 2, 1 and 4, 2, 2: 16; 1, 2, 1: 12.
 namespace f32 {
 constexpr int KEYS = 64;
 constexpr int STAGES = 2;
