@@ -29,7 +29,8 @@ class GPT:
         self.device = torch.device(device)
         self.weights = native.pack_weights(cfg, tensors, self.device)
         self._ws = None
-        self._ws_bt = None
+        self._ws_captured = False   # a graph may hold its address
+        self._ws_replaced = []      # ... of these too
         self._host = {}
 
     def workspace(self, B: int, T: int) -> torch.Tensor:
@@ -37,7 +38,10 @@ class GPT:
         if need == 0:
             raise native.GPTError(native.GPT_ERR_BAD_SHAPE, "gpt_workspace_bytes")
         if self._ws is None or self._ws.numel() < need:
-            self._ws = native.alloc_workspace(need, self.device)
+            if self._ws_captured:
+                self._ws_replaced.append(self._ws)
+            self._ws, self._ws_captured = native.alloc_workspace(need, self.device), False
+        self._ws_captured |= torch.cuda.is_current_stream_capturing()
         return self._ws
 
     def __call__(self, idx, targets=None, **kw):

@@ -633,3 +633,34 @@ def test_verify_and_score_of_a_padded_vocabulary():
             m.score(idx.cuda(), tgt.cuda(), vocab=bad)
         with pytest.raises(ValueError):
             m.verify(tok, par, lens, kv, vocab=bad)
+
+
+def test_captured_calls_outlive_a_larger_workspace():
+    """A recorded GPT.verify and forward stay right, and write into nobody else's memory, after a larger call has
+    replaced the model's workspace."""
+    from decoder_only_transformer_causal_b200 import native
+    B, T0, N = 2, 10, 5
+    m, cfg, _, prompt, kv = tree_model("tiny", None, B, T0)
+    kv0 = kv.clone()
+    par = torch.tensor([[-1, 0, 1, 0, 3]] * B, dtype=torch.int32, device="cuda")
+    tok = torch.randint(0, 65, (B, N), generator=torch.Generator().manual_seed(1)).cuda()
+    lens = torch.full((B,), T0, dtype=torch.int32, device="cuda")
+    want, chosen = m.verify(tok, par, lens, kv)
+    want, after = [t.clone() for t in (*want, chosen)], kv.clone()
+    logits, _ = m(tok, tok)
+    logits = logits.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        acc, got = m.verify(tok, par, lens, kv)
+        z, _ = m(tok, tok)
+    size = m.workspace(B, N).numel()
+    idx = torch.zeros((64, 64), dtype=torch.int64, device="cuda")
+    m(idx, idx)                                       # a larger workspace
+    assert m.workspace(B, N).numel() > size
+    canaries = [torch.full((size,), 7, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    for _ in range(2):
+        kv.copy_(kv0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*acc, got), want)) and torch.equal(kv, after) and torch.equal(z, logits)
+        assert all((c == 7).all() for c in canaries)
