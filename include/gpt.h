@@ -128,7 +128,7 @@ int gpt_check_status(void* workspace, void* stream);
  * wait gives up records GPT_ERR_TIMEOUT in its status word, lets every copy and product it has
  * already issued finish (those drains keep the default limit), releases its tensor memory and
  * returns; its outputs are then invalid.
- *   force_timeout != 0 makes the causal attention kernel, the product kernels (gpt_linear,
+ *   force_timeout != 0 makes the causal attention kernel, those of gpt_tree_attention, the product kernels (gpt_linear,
  *   single CTAs for M < 256 and CTA pairs from M = 256) and the single-launch decode step
  *   (gpt_decode_step and gpt_generate in bf16, at its first grid barrier) launched from then on
  *   wait first for an event that never happens, so their time-out path runs on purpose after
@@ -349,6 +349,8 @@ int gpt_generate(const gpt_config_t* cfg, const void* weights, const int64_t* id
  *           fp32 numbers to 5 x 2^-22 of it, as three TF32 products; fp32 sums).
  *   N = 1 with parent -1 is the attention of an ordinary decode step with a length per sequence.
  *   status  optional device int32 (NULL allowed), never cleared by the library.
+ * The sums of p v are taken before the division by the sum of p, with p up to 2^8 in bf16 and 1 in fp32: values
+ * near the type's largest may overflow.
  * No workspace; results are bit-reproducible. */
 int gpt_tree_attention(const void* qkv, const void* kv, const int32_t* lengths, const int32_t* parents,
                        void* y, int B, int N, int nh, int hs, int block_size, int dtype,
@@ -389,7 +391,7 @@ int gpt_tree_accept(const gpt_config_t* cfg, const int32_t* parents, const int64
 
 /* ---- log probabilities of given tokens --------------------------------------------------
  * The per-position terms of "nanoGPT 全局流程图" §3.3 (logsumexp(z) - z[target]) for scoring, ranking and
- * policy-gradient training: with z = logits[r, 0..V) / temperature and p = softmax(z),
+ * objectives on log probabilities: with z = logits[r, 0..V) / temperature and p = softmax(z),
  *   lse[r]      = log sum_v exp(z_v)
  *   logp[r]     = z[tokens[r]] - lse[r], 0 where tokens[r] == -1
  *   entropy[r]  = -sum_v p_v log p_v  (0 log 0 = 0)
@@ -414,7 +416,8 @@ int gpt_token_logprobs(const void* logits, long long ld, const int64_t* tokens, 
  * lse (and, with dentropy, entropy) as gpt_token_logprobs wrote them.  dlogp NULL: no such term (tokens
  * may be NULL); dentropy NULL: none (entropy may be NULL).  dlogp counts as 0 where tokens[r] == -1 (and
  * where it is out of range, with GPT_ERR_INDEX).  Rows whose two factors are 0 are written as zeros and
- * their logits are not read.  Logits of -inf get 0.
+ * their logits are not read.  Logits of -inf get 0, as do all whose probability rounds to 0; the token's own
+ * term dlogp / temperature comes on top.  A row whose lse is NaN or +inf is written as NaN, one with lse -inf as zeros.
  * dlogits [rows, ldd] in `dtype` (ldd >= V; columns from V on are left as they are); it may be the logits
  * buffer itself with ldd == ld. */
 int gpt_token_logprobs_backward(const void* logits, long long ld, const int64_t* tokens, int rows, int V,
