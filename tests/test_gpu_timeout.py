@@ -183,3 +183,27 @@ def test_fp32_tree_attention_wait_limit_gives_timeout_then_recovers(short_waits,
         ref = (torch.softmax(s, -1) @ x[:, 1].transpose(0, 1)).transpose(0, 1).reshape(N, nh * hs)
         # 2 a ((hs + 28) u D + (n + N + 28) u) of test_gpu_tree's tolerance with hs 128, D 10, n 1100, a 1
         assert float((y[b] - ref).abs().max()) <= 4e-4
+
+
+@pytest.mark.parametrize("N", [16, 17, 32, 33, 64])
+def test_tree_attention_of_paired_warps_ends_after_a_timeout(short_waits, N):
+    """Warps that exchange their weights' parts at a barrier of two leave the steps, and the rounds, together."""
+    native = short_waits
+    B, nh = 40, 16
+    g = torch.Generator(device="cuda").manual_seed(75)
+    qkv = torch.randn((B, N, 3, nh * 64), generator=g, device="cuda").to(torch.bfloat16)
+    qkv[:, :, 2] = 0.75
+    kv = torch.randn((B, 400, 2, nh * 64), generator=g, device="cuda").to(torch.bfloat16)
+    kv[:, :, 1] = 0.75
+    lens = (torch.arange(B, dtype=torch.int32, device="cuda") * 10)
+    par = torch.arange(-1, N - 1, dtype=torch.int32, device="cuda").repeat(B, 1)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    native.tree_attention(qkv, kv, lens, par, nh, status=st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == native.GPT_ERR_TIMEOUT
+    native.set_wait_limit_ns(0)
+    st.zero_()
+    y = native.tree_attention(qkv, kv, lens, par, nh, status=st)
+    torch.cuda.synchronize()
+    # values all alike: their mean is the value, whatever the weights (sums off by 2^-15, which rounding to bf16 hides)
+    assert int(st.item()) == native.GPT_OK and (y == 0.75).all()
