@@ -105,6 +105,8 @@ class GPT:
         range (else that is in native.check_status(model.workspace(B, T)))."""
         B, T = idx.shape
         vocab = self._vocab(vocab)
+        for name, t in (("idx", idx), ("targets", targets)):   # before the forward reads them
+            native.check_tensor(name, t, torch.int64, (B, T), self.weights.device)
         ws = self.workspace(B, T)
         logits, _ = self(idx, targets)
         r = native.token_logprobs(logits.view(B * T, -1)[:, :vocab], targets.reshape(-1), k=k, temperature=temperature,

@@ -518,6 +518,11 @@ def _arg(name: str, t: torch.Tensor, dtype, shape, device) -> int:
     raise ValueError(f"{name} must be contiguous")
 
 
+def check_tensor(name: str, t: torch.Tensor, dtype, shape, device) -> None:
+    """Raises ValueError unless t is a contiguous tensor of the given dtype, shape and device."""
+    _arg(name, t, dtype, shape, device)
+
+
 def _status_arg(status, device):
     return None if status is None else _arg("status", status, torch.int32, status.shape, device)
 

@@ -155,6 +155,24 @@ def test_sizes_past_the_calls_integers_are_refused(shape):
         native.token_logprobs_backward(z, None, torch.empty(shape[0], device="meta"))
 
 
+def test_score_checks_its_tensors_before_the_forward():
+    """The forward reads B T 64-bit integers from idx and from targets: others are refused before it is launched."""
+    from decoder_only_transformer_causal_b200 import GPT
+    m = GPT.__new__(GPT)
+    m.cfg, m.weights = _cfg(), torch.empty(1)
+
+    def launched(*a):
+        raise AssertionError("the forward was reached")
+    m.workspace = launched
+    idx = torch.zeros((2, 9), dtype=torch.int64)
+    with pytest.raises(AssertionError, match="reached"):
+        m.score(idx, idx)
+    for a, b in ((idx, idx[:, :8].contiguous()), (idx, idx.int()), (idx.int(), idx), (idx, idx.view(-1)), (idx, idx[:1]),
+                 (idx, torch.zeros((9, 2), dtype=torch.int64).t()), (idx, idx.to("meta"))):
+        with pytest.raises(ValueError):
+            m.score(a, b)
+
+
 # ------------------------------------------------------------------ the definitions themselves
 def test_see_sets():
     par = np.array([[-1, 0, 0, 1, 3, -2, 5, 9, -1, 8]])
